@@ -13,12 +13,19 @@ Beyond them: wall_attn_fwd / wall_attn_bwd (the two halves, from P),
 wall_attn_fwd_gate (prefix scan fused into the forward), wall_attn_decode_chunk
 (several queries against the cache: multi-token decode, chunked prefill) and
 WallAttnStepGraph (a training step captured in a CUDA graph).
+Paged cache (requests of different lengths sharing pools of pages):
+WallPagedTables and WallPagedCache, over wall_paged_plan, wall_paged_append,
+wall_paged_attn and wall_paged_release.
 The C-ABI calls are also exposed one to one in ``channel_decay_softmax_b200._lib``.
 """
-from .api import (WallAttnFunction, WallAttnStepGraph, WallDecodeCache, build_wall_kv_cache,
-                  prefix_cumsum, wall_attn, wall_attn_bwd, wall_attn_decode,
-                  wall_attn_decode_chunk, wall_attn_fwd, wall_attn_fwd_gate)
+from .api import (WallAttnFunction, WallAttnStepGraph, WallDecodeCache, WallPagedCache,
+                  WallPagedPlan, WallPagedTables, build_wall_kv_cache, prefix_cumsum, wall_attn,
+                  wall_attn_bwd, wall_attn_decode, wall_attn_decode_chunk, wall_attn_fwd,
+                  wall_attn_fwd_gate, wall_paged_append, wall_paged_attn, wall_paged_plan,
+                  wall_paged_release)
 
 __all__ = ["wall_attn", "wall_attn_fwd", "wall_attn_fwd_gate", "wall_attn_bwd", "prefix_cumsum",
            "build_wall_kv_cache", "wall_attn_decode", "wall_attn_decode_chunk",
-           "WallAttnFunction", "WallAttnStepGraph", "WallDecodeCache"]
+           "WallAttnFunction", "WallAttnStepGraph", "WallDecodeCache", "wall_paged_plan",
+           "wall_paged_release", "wall_paged_append", "wall_paged_attn", "WallPagedPlan",
+           "WallPagedTables", "WallPagedCache"]

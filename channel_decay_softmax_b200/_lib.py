@@ -25,6 +25,9 @@ EXPORTS = ["wall_version", "wall_error_string", "wall_prefix_cumsum", "wall_attn
            "wall_attn_decode_chunk_workspace", "wall_attn_decode_chunk",
            "wall_attn_fwd_gate_workspace", "wall_attn_fwd_gate", "wall_timing_enable_slots",
            "wall_attn_bwd_workspace_min"]
+# declared in wall_paged.h
+PAGED_EXPORTS = ["wall_paged_plan", "wall_paged_release", "wall_paged_append_workspace",
+                 "wall_paged_append", "wall_paged_attn_workspace", "wall_paged_attn"]
 
 _lib = None
 
@@ -99,6 +102,21 @@ def lib():
         L.wall_attn_decode_chunk.restype = i
         L.wall_attn_decode_chunk.argtypes = [vp, vp, fp, vp, fp, fp, f, i, i, i, i, i, i, i, i,
                                              i, i, vp, fp, vp, sz, vp]
+        L.wall_paged_plan.restype = i
+        L.wall_paged_plan.argtypes = [ip, ip, ip, ip, ip, i, i, i, i, i, ip, ip, vp, ip, ip, ip,
+                                      vp]
+        L.wall_paged_release.restype = i
+        L.wall_paged_release.argtypes = [ip, ip, ip, ip, ip, i, i, i, i, vp]
+        L.wall_paged_append_workspace.restype = sz
+        L.wall_paged_append_workspace.argtypes = [i, i, i, i, i, i]
+        L.wall_paged_append.restype = i
+        L.wall_paged_append.argtypes = [vp, vp, vp, i, ip, ip, vp, i, i, i, i, i, i, i, i, i, vp,
+                                        vp, ip, vp, vp, fp, vp, sz, vp]
+        L.wall_paged_attn_workspace.restype = sz
+        L.wall_paged_attn_workspace.argtypes = [i, i, i, i, i, i, i, i]
+        L.wall_paged_attn.restype = i
+        L.wall_paged_attn.argtypes = [vp, fp, i, ip, ip, ip, i, i, i, i, i, i, i, i, i, i, vp, vp,
+                                      ip, fp, f, i, vp, fp, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -259,3 +277,60 @@ def wall_attn_fwd_gate(q, k, v, g, B, T, H, HQ, K, V, scale, g_scalar, sink_bias
         _p(q), _p(k), _p(v), _p(g), dtype_code(q.dtype), B, T, H, HQ, K, V, float(scale),
         _p(g_scalar), _p(sink_bias), int(window_size), _p(cu_seqlens), n_seq, _p(P), _p(o),
         _p(lse), _p(workspace), ws_bytes, _stream(stream)))
+
+
+# The paged calls run on the device that holds their tensors, whatever the
+# current one, on that device's current stream unless one is given.
+def _on_device(t, fn, *args, stream=None):
+    if t.device.index == torch.cuda.current_device():
+        return fn(*args, _stream(stream))
+    with torch.cuda.device(t.device):
+        return fn(*args, _stream(stream))
+
+
+def wall_paged_plan(new_lens, lens, block_table, free_list, free_count, n_req, max_pages,
+                    num_pages, page_size, n_tokens, cu_q, kv_lens, slot_map, admitted, lens_out,
+                    free_count_out, stream=None):
+    _check("wall_paged_plan", _on_device(
+        cu_q, lib().wall_paged_plan, _p(new_lens), _p(lens), _p(block_table), _p(free_list),
+        _p(free_count), n_req, max_pages, num_pages, page_size, n_tokens, _p(cu_q), _p(kv_lens),
+        _p(slot_map), _p(admitted), _p(lens_out), _p(free_count_out), stream=stream))
+
+
+def wall_paged_release(finished, lens, block_table, free_list, free_count, n_req, max_pages,
+                       num_pages, page_size, stream=None):
+    _check("wall_paged_release", _on_device(
+        free_list, lib().wall_paged_release, _p(finished), _p(lens), _p(block_table),
+        _p(free_list), _p(free_count), n_req, max_pages, num_pages, page_size, stream=stream))
+
+
+def wall_paged_append_workspace(n_req, n_tokens, max_new, HQ, K, page_size) -> int:
+    return lib().wall_paged_append_workspace(n_req, n_tokens, max_new, HQ, K, page_size)
+
+
+def wall_paged_append(k, v, g, cu_q, kv_lens, slot_map, n_req, n_tokens, max_new, H, HQ, K, V,
+                      page_size, num_pages, k_pages, v_pages, r_pages, carry_in, carry_out, p,
+                      workspace=None, stream=None):
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("wall_paged_append", _on_device(
+        k_pages, lib().wall_paged_append, _p(k), _p(v), _p(g), dtype_code(k_pages.dtype),
+        _p(cu_q), _p(kv_lens), _p(slot_map), n_req, n_tokens, max_new, H, HQ, K, V, page_size,
+        num_pages, _p(k_pages), _p(v_pages), _p(r_pages), _p(carry_in), _p(carry_out), _p(p),
+        _p(workspace), ws_bytes, stream=stream))
+
+
+def wall_paged_attn_workspace(dtype, n_req, n_tokens, max_new, H, HQ, K, V) -> int:
+    return lib().wall_paged_attn_workspace(dtype_code(dtype), n_req, n_tokens, max_new, H, HQ, K,
+                                           V)
+
+
+def wall_paged_attn(q, p, cu_q, kv_lens, block_table, n_req, n_tokens, max_new, max_pages, H, HQ,
+                    K, V, page_size, num_pages, k_pages, v_pages, r_pages, sink_bias, scale,
+                    window_size, o, lse, workspace, stream=None):
+    """New tokens' attention over the paged cache."""
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("wall_paged_attn", _on_device(
+        k_pages, lib().wall_paged_attn, _p(q), _p(p), dtype_code(k_pages.dtype), _p(cu_q),
+        _p(kv_lens), _p(block_table), n_req, n_tokens, max_new, max_pages, H, HQ, K, V, page_size,
+        num_pages, _p(k_pages), _p(v_pages), _p(r_pages), _p(sink_bias), float(scale),
+        int(window_size), _p(o), _p(lse), _p(workspace), ws_bytes, stream=stream))

@@ -7,6 +7,8 @@ of the computation runs in libwall.so's CUDA kernels.
 """
 from __future__ import annotations
 
+from typing import NamedTuple
+
 import torch
 
 from . import _lib as L
@@ -468,6 +470,256 @@ class WallDecodeCache:
                            o, lse, self.step_ws)
         self.length = t + 1
         return o, lse
+
+
+# ---------------------------------------------------------------------------
+# Paged cache: requests of different lengths share pools of pages.
+
+PAGE_SIZES = (32, 64, 128)
+
+
+class WallPagedPlan(NamedTuple):
+    """Where a step's tokens go: row offsets cu_q [N+1] and kv_lens [N]
+    (cached tokens after the step, 0 for a request that was refused), int32;
+    slot_map [n_tokens] int64, page * page_size + offset of every packed row
+    (-1: none); admitted [N] int32."""
+    cu_q: torch.Tensor
+    kv_lens: torch.Tensor
+    slot_map: torch.Tensor
+    admitted: torch.Tensor
+
+
+def _page_size(n):
+    if n not in PAGE_SIZES:
+        raise ValueError(f"page_size must be one of {PAGE_SIZES}, got {n}")
+    return int(n)
+
+
+def _tables(lens, block_table, free_list, free_count):
+    """Shapes of the page bookkeeping; returns (N, max_pages, num_pages)."""
+    if lens.dim() != 1 or block_table.dim() != 2 or free_list.dim() != 1:
+        raise ValueError("lens must be [N], block_table [N, max_pages], free_list [num_pages]")
+    N, MP = lens.shape[0], block_table.shape[1]
+    _expect("lens", lens, (N,), torch.int32)
+    _expect("block_table", block_table, (N, MP), torch.int32)
+    _expect("free_list", free_list, (free_list.shape[0],), torch.int32)
+    _expect("free_count", free_count, (1,), torch.int32)
+    _same_device(lens, block_table, free_list, free_count)
+    return N, MP, free_list.shape[0]
+
+
+def wall_paged_plan(new_lens, lens, block_table, free_list, free_count, page_size, n_tokens,
+                    lens_out=None, free_count_out=None):
+    """Plans a serving step on the GPU: request i, with lens[i] cached tokens,
+    brings new_lens[i] more (0: none), packed back to back into n_tokens rows.
+
+    Opens the pages they need beyond the ones held, from the top of the stack
+    free_list[:free_count] and in request order, writes their ids into
+    block_table (in place), and returns a WallPagedPlan.  A request whose
+    pages exceed the stack (with those before it) or its table row, or whose
+    rows exceed n_tokens, is refused: nothing of it changes, its slots are -1
+    and its kv_len 0.  lens and free_count are updated in place unless lens_out
+    / free_count_out are given.  No host synchronization; may be captured."""
+    PS = _page_size(page_size)
+    N, MP, NP = _tables(lens, block_table, free_list, free_count)
+    n_tokens = int(n_tokens)
+    if n_tokens < 0 or MP < 1 or NP < 1:
+        raise ValueError("need n_tokens >= 0, a block table of at least one page and a pool")
+    _expect("new_lens", new_lens, (N,), torch.int32)
+    lens_out = lens if lens_out is None else lens_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    _expect("lens_out", lens_out, (N,), torch.int32)
+    _expect("free_count_out", free_count_out, (1,), torch.int32)
+    _same_device(lens, new_lens, lens_out, free_count_out)
+    dev = lens.device
+    cu_q = torch.empty(N + 1, dtype=torch.int32, device=dev)
+    kv_lens = torch.empty(N, dtype=torch.int32, device=dev)
+    slot_map = torch.empty(n_tokens, dtype=torch.int64, device=dev)
+    admitted = torch.empty(N, dtype=torch.int32, device=dev)
+    L.wall_paged_plan(new_lens, lens, block_table, free_list, free_count, N, MP, NP, PS, n_tokens,
+                      cu_q, kv_lens, slot_map, admitted, lens_out, free_count_out)
+    return WallPagedPlan(cu_q, kv_lens, slot_map, admitted)
+
+
+def wall_paged_release(finished, lens, block_table, free_list, free_count, page_size):
+    """Returns the pages of the requests with finished[i] != 0 (int32 [N]) to
+    the stack, in place; their table rows become -1 and their lengths 0."""
+    PS = _page_size(page_size)
+    N, MP, NP = _tables(lens, block_table, free_list, free_count)
+    _expect("finished", finished, (N,), torch.int32)
+    _same_device(lens, finished)
+    if MP < 1 or NP < 1:
+        raise ValueError("need a block table of at least one page and a pool")
+    L.wall_paged_release(finished, lens, block_table, free_list, free_count, N, MP, NP, PS)
+
+
+def _pools(k_pages, v_pages, r_pages):
+    """Shapes of one layer's pools; returns (num_pages, page_size, H, HQ, K, V)."""
+    if k_pages.dim() != 4 or v_pages.dim() != 4:
+        raise ValueError("k_pages must be [num_pages, HQ, page_size, K] and v_pages "
+                         "[num_pages, H, page_size, V]")
+    NP, HQ, PS, K = k_pages.shape
+    H, V = v_pages.shape[1], v_pages.shape[3]
+    _page_size(PS)
+    _io_dtype(k_pages, v_pages)
+    if v_pages.shape[0] != NP or v_pages.shape[2] != PS or H < 1 or HQ % H != 0:
+        raise ValueError("v_pages must be [num_pages, H, page_size, V] with k_pages' pages and "
+                         "HQ % H == 0")
+    _expect("r_pages", r_pages, (NP, HQ, K), torch.int32)
+    _same_device(k_pages, v_pages, r_pages)
+    return NP, PS, H, HQ, K, V
+
+
+def _batch(cu_q, kv_lens, max_new, T):
+    """The ragged batch's N and the bound on a request's rows (default: T)."""
+    if kv_lens.dim() != 1:
+        raise ValueError("kv_lens must be [N]")
+    N = kv_lens.shape[0]
+    _expect("kv_lens", kv_lens, (N,), torch.int32)
+    _expect("cu_q", cu_q, (N + 1,), torch.int32)
+    max_new = T if max_new is None else int(max_new)
+    if max_new < 1 and T > 0:
+        raise ValueError("max_new must be positive")
+    return N, min(max_new, T)
+
+
+def wall_paged_append(k, v, g, cu_q, kv_lens, slot_map, k_pages, v_pages, r_pages, carry,
+                      carry_out=None, max_new=None):
+    """Appends a step's packed tokens k [T,H,K], v [T,H,V], g [T,HQ,K] to the
+    pools at the rows of slot_map (a plan's) and returns p [T,HQ,K] fp32, each
+    token's gate prefix beyond its page's anchor, which wall_paged_attn takes.
+
+    carry int64 [N,HQ,K] is each request's prefix in 2^-24 powers of two (its
+    value does not matter where nothing is cached yet), updated in place unless
+    carry_out is given.  max_new: a bound on a request's new tokens, when the
+    caller knows one.  The state after an append does not depend on how the
+    tokens were cut into calls, bit for bit.  Rows past cu_q[N] and those of
+    refused requests are not read, nor their p written."""
+    NP, PS, H, HQ, K, V = _pools(k_pages, v_pages, r_pages)
+    if k.dim() != 3:
+        raise ValueError("k must be [T, H, K]")
+    T = k.shape[0]
+    _io_dtype(k_pages, k, v, g)
+    _expect("k", k, (T, H, K))
+    _expect("v", v, (T, H, V))
+    _expect("g", g, (T, HQ, K))
+    _expect("slot_map", slot_map, (T,), torch.int64)
+    N, max_new = _batch(cu_q, kv_lens, max_new, T)
+    carry_out = carry if carry_out is None else carry_out
+    _expect("carry", carry, (N, HQ, K), torch.int64)
+    _expect("carry_out", carry_out, (N, HQ, K), torch.int64)
+    _same_device(k_pages, k, v, g, cu_q, kv_lens, slot_map, carry, carry_out)
+    p = torch.empty((T, HQ, K), dtype=torch.float32, device=k_pages.device)
+    nbytes = L.wall_paged_append_workspace(N, T, max_new, HQ, K, PS)
+    ws = _ws(nbytes, k_pages.device) if nbytes else None
+    L.wall_paged_append(k.contiguous(), v.contiguous(), g.contiguous(), cu_q, kv_lens, slot_map,
+                        N, T, max_new, H, HQ, K, V, PS, NP, k_pages, v_pages, r_pages, carry,
+                        carry_out, p, ws)
+    return p
+
+
+def wall_paged_attn(q, p, cu_q, kv_lens, block_table, k_pages, v_pages, r_pages, max_new=None,
+                    scale=None, sink_bias=None, window_size=None, return_lse=False):
+    """Attention of packed query rows over the paged cache: rows
+    cu_q[i]:cu_q[i+1] of q [T,HQ,K] are the last positions of request i's
+    kv_lens[i] cached ones and see them causally (within window_size, if
+    given); p [T,HQ,K] is what wall_paged_append returned for them.  Returns
+    o [T,HQ,V], or (o, lse [T,HQ] fp32) with return_lse.
+
+    One token a request, several, whole prompts and mixtures of them take the
+    same call.  max_new: a bound on a request's rows, when the caller knows
+    one (1 for a plain decode step, which then launches less).  A request with
+    fewer cached tokens than rows (refused: 0) sees nothing: o = 0, lse = -inf
+    (the sink's bias, if there is one).  Rows past cu_q[N] are left as they
+    are."""
+    NP, PS, H, HQ, K, V = _pools(k_pages, v_pages, r_pages)
+    if q.dim() != 3:
+        raise ValueError("q must be [T, HQ, K]")
+    T = q.shape[0]
+    _io_dtype(k_pages, q)
+    _expect("q", q, (T, HQ, K))
+    _expect("p", p, (T, HQ, K), torch.float32)
+    N, max_new = _batch(cu_q, kv_lens, max_new, T)
+    if block_table.dim() != 2 or block_table.shape[1] < 1:
+        raise ValueError("block_table must be [N, max_pages]")
+    MP = block_table.shape[1]
+    _expect("block_table", block_table, (N, MP), torch.int32)
+    sk = _opt_f32("sink_bias", sink_bias, (HQ,))
+    _same_device(k_pages, q, p, cu_q, kv_lens, block_table, sk)
+    dev = k_pages.device
+    o = torch.empty((T, HQ, V), dtype=q.dtype, device=dev)
+    lse = torch.empty((T, HQ), dtype=torch.float32, device=dev) if return_lse else None
+    ws = _ws(L.wall_paged_attn_workspace(q.dtype, N, T, max_new, H, HQ, K, V), dev)
+    L.wall_paged_attn(q.contiguous(), p.contiguous(), cu_q, kv_lens, block_table, N, T, max_new,
+                      MP, H, HQ, K, V, PS, NP, k_pages, v_pages, r_pages, sk, scale or 0.0,
+                      window_size or 0, o, lse, ws)
+    return (o, lse) if return_lse else o
+
+
+class WallPagedTables:
+    """The page bookkeeping of a serving batch, all on the GPU: N request rows
+    of up to max_pages pages each, out of a pool of num_pages.  One serves
+    every layer's WallPagedCache, since their pages are opened together."""
+
+    def __init__(self, n_requests, max_pages, num_pages, page_size=64, device="cuda"):
+        if n_requests < 1 or max_pages < 1 or num_pages < 1:
+            raise ValueError("need at least one request, one page a request and one page")
+        self.page_size, self.num_pages = _page_size(page_size), int(num_pages)
+        self.lens = torch.zeros(n_requests, dtype=torch.int32, device=device)
+        self.block_table = torch.full((n_requests, max_pages), -1, dtype=torch.int32,
+                                      device=device)
+        # a stack: its top is the last entry, page 0 is opened first
+        self.free_list = torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device)
+        self.free_count = torch.full((1,), num_pages, dtype=torch.int32, device=device)
+
+    def plan(self, new_lens, n_tokens):
+        """The plan of a step that brings new_lens[i] tokens of each request."""
+        return wall_paged_plan(new_lens, self.lens, self.block_table, self.free_list,
+                               self.free_count, self.page_size, n_tokens)
+
+    def release(self, finished):
+        """Finished requests' pages back to the pool; their rows start empty."""
+        wall_paged_release(finished, self.lens, self.block_table, self.free_list,
+                           self.free_count, self.page_size)
+
+
+class WallPagedCache:
+    """One layer's paged decode state: the pools of the tables' pages and each
+    request's running prefix.
+
+        tables = WallPagedTables(n_requests, max_pages, num_pages)
+        cache = WallPagedCache(tables, H, HQ, K, V)          # one per layer
+        plan = tables.plan(new_lens, n_tokens)                # once a step
+        o = cache.step(plan, q, k, v, g)                      # each layer
+    """
+
+    def __init__(self, tables, H, HQ, K, V, dtype=torch.bfloat16, scale=None, sink_bias=None,
+                 window_size=None):
+        if H < 1 or HQ % H != 0:
+            raise ValueError("need HQ % H == 0")
+        dev = tables.lens.device
+        NP, PS = tables.num_pages, tables.page_size
+        self.tables, self.scale, self.window = tables, scale, window_size
+        self.sink = _opt_f32("sink_bias", sink_bias, (HQ,))
+        self.k_pages = torch.empty((NP, HQ, PS, K), dtype=dtype, device=dev)
+        self.v_pages = torch.empty((NP, H, PS, V), dtype=dtype, device=dev)
+        self.r_pages = torch.empty((NP, HQ, K), dtype=torch.int32, device=dev)
+        self.carry = torch.zeros((tables.lens.shape[0], HQ, K), dtype=torch.int64, device=dev)
+
+    def append(self, plan, k, v, g, max_new=None):
+        """The plan's packed tokens into the pools; returns their p."""
+        return wall_paged_append(k, v, g, plan.cu_q, plan.kv_lens, plan.slot_map, self.k_pages,
+                                 self.v_pages, self.r_pages, self.carry, max_new=max_new)
+
+    def attend(self, plan, q, p, max_new=None, return_lse=False):
+        """The plan's query rows over their requests' cached tokens."""
+        return wall_paged_attn(q, p, plan.cu_q, plan.kv_lens, self.tables.block_table,
+                               self.k_pages, self.v_pages, self.r_pages, max_new, self.scale,
+                               self.sink, self.window, return_lse)
+
+    def step(self, plan, q, k, v, g, max_new=None, return_lse=False):
+        """append, then attend."""
+        return self.attend(plan, q, self.append(plan, k, v, g, max_new), max_new, return_lse)
 
 
 def timing_enable(on=True):

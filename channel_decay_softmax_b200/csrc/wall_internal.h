@@ -221,4 +221,46 @@ int decode_step(const void* q, const void* k, const void* v, const void* g, floa
                 int C, int t, int B, int Tcap, int H, int HQ, int K, int V, void* o, float* lse,
                 float* ws, unsigned* counters, int splits, cudaStream_t stream);
 
+// ---- paged cache (wall_paged_plan.cu, wall_paged_append.cu, wall_paged_attn.cu);
+// shift: log2 of the page size ----
+int paged_plan(const int* new_lens, const int* lens, int* table, const int* free_list,
+               const int* free_count, int N, int MP, int NP, int shift, int T, int* cu, int* kv,
+               int64_t* slots, int* admitted, int* lens_out, int* free_out, cudaStream_t stream);
+int paged_release(const int* finished, int* lens, int* table, int* free_list, int* free_count,
+                  int N, int MP, int NP, int shift, cudaStream_t stream);
+
+struct PagedAppendProblem {
+  const void *k, *v, *g;
+  int dtype;
+  const int *cu, *kv;
+  const int64_t* slots;
+  int N, T, max_new;  // requests, packed rows, most rows of a request
+  int H, HQ, K, V, shift, NP;
+  void *k_pages, *v_pages;
+  int* r_pages;
+  const int64_t* carry_in;
+  int64_t* carry_out;
+  float* p;
+};
+size_t paged_append_ws(int N, int T, int HQ, int K, int shift, int max_new);
+int paged_append(const PagedAppendProblem& pb, void* ws, cudaStream_t stream);
+
+struct PagedAttnProblem {
+  const void* q;
+  const float* p;
+  int dtype;
+  const int *cu, *kv, *table;
+  int N, T, MP, max_new;
+  int H, HQ, K, V, shift, NP;
+  const void *k_pages, *v_pages;
+  const int* r_pages;
+  const float* sink;
+  float scale;
+  int window;
+  void* o;
+  float* lse;
+};
+size_t paged_attn_ws(int dtype, int N, int T, int max_new, int H, int HQ, int K, int V);
+int paged_attn(const PagedAttnProblem& pb, void* ws, cudaStream_t stream);
+
 }  // namespace wall

@@ -1,0 +1,351 @@
+// wall_paged_attn.cu -- attention of new tokens over the paged Wall cache: the
+// general kernel (any dtype and head size), the join of units that two or more
+// CTAs share, and the choice of kernels.
+//
+//   s_ij = scale sum_n q_in 2^(p_in + R_{page(i),n} - R_{page(j),n}) k_jn
+//   o_i  = sum_j softmax(s_i, sink)_j v_j,   j <= i, i - j < window
+// where k_jn is the cached row (k 2^(R - P)), p the token's prefix beyond its
+// page's anchor and R the pages' whole-number anchors: the query meets each
+// page once, scaled, and the inner loop has no gate arithmetic.
+#include "wall_paged_attn.h"
+
+namespace wall {
+namespace {
+
+using namespace paged;
+
+// ---------------------------------------------------------------------------
+// general kernel: 32 query rows of one head against tiles of 32 keys, fp32
+// throughout.  Four warps of eight rows; lane = key for the scores (a key's
+// channels from shared memory, the rows' by broadcast: one load of keys feeds
+// eight rows), then lane = four value channels for P V.
+
+constexpr int GR = kGeneralRows;
+constexpr int kGenWarps = 4, kGenThreads = kGenWarps * 32;
+constexpr int kRowsPerWarp = GR / kGenWarps;
+
+size_t gen_smem(int K, int V) { return sizeof(float) * (size_t)(GR * K + GR * (K + 4) + GR * V); }
+
+// Tiles [ta, tb) of the row block: softmax state of this warp's rows.
+template <typename T>
+__device__ __forceinline__ void gen_tiles(const AttnArgs& a, const Request& r, int h, int row0,
+                                          int lo_tile, int ta, int tb, float* smem,
+                                          float (&m)[kRowsPerWarp], float (&l)[kRowsPerWarp],
+                                          float (&acc)[kRowsPerWarp][4]) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int K = a.K, V = a.V;
+  float* sQ = smem;              // [GR][K]
+  float* sK = sQ + GR * K;       // [GR][K + 4]
+  float* sV = sK + GR * (K + 4); // [GR][V]
+  const T* q = static_cast<const T*>(a.q);
+  const T* kp = static_cast<const T*>(a.kp);
+  const T* vp = static_cast<const T*>(a.vp);
+  const int kh = h / (a.HQ / a.H);
+  const long trow = (long)r.i * a.MP;
+  const int ni = min(GR, r.n - row0);
+  const int win = a.window > 0 ? a.window : 0x7fffffff;
+  const int w0 = warp * kRowsPerWarp;
+#pragma unroll
+  for (int x = 0; x < kRowsPerWarp; ++x) {
+    m[x] = -INFINITY;
+    l[x] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[x][e] = 0.f;
+  }
+  if (r.dead) return;
+  int at = -1;  // table slot whose scaled queries are in sQ
+  for (int t = ta; t < tb; ++t) {
+    const int j0 = (lo_tile + t) * GR;
+    const int slot = j0 >> a.shift;
+    const int page = slot < a.MP ? page_of(a.table, trow, slot, a.NP) : -1;
+    if (page < 0) {  // the same for the whole CTA: an entry outside the pool
+      if (tid == 0) record_status(a.status, WALL_ERR_INVALID_ARG);
+      continue;
+    }
+    __syncthreads();  // the last tile's readers are done
+    if (slot != at) {
+      const int* Rc = a.rp + ((long)page * a.HQ + h) * K;
+      for (int idx = tid; idx < GR * K; idx += kGenThreads) {
+        const int row = idx / K, c = idx - row * K;
+        float x = 0.f;
+        if (row < ni) {
+          const int rs = (r.ctx + row0 + row) >> a.shift;
+          if (rs >= slot) {  // rows of an earlier page see nothing of this one
+            const int rpage = rs < a.MP ? page_of(a.table, trow, rs, a.NP) : -1;
+            const int Rr = rpage >= 0 ? a.rp[((long)rpage * a.HQ + h) * K + c] : 0;
+            const long e = ((long)(r.t0 + row0 + row) * a.HQ + h) * K + c;
+            x = a.scale_log2 * to_f32(q[e]) * exp2f(a.p[e] + (float)(Rr - Rc[c]));
+          }
+        }
+        sQ[idx] = x;
+      }
+      at = slot;
+    }
+    const int off = j0 & ((1 << a.shift) - 1);
+    const T* kt = kp + ((((long)page * a.HQ + h) << a.shift) + off) * K;
+    const T* vt = vp + ((((long)page * a.H + kh) << a.shift) + off) * V;
+    for (int idx = tid; idx < GR * (K / 8); idx += kGenThreads) {
+      const int j = idx / (K / 8), c = (idx - j * (K / 8)) * 8;
+      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (j0 + j < r.kv) load8(kt + (long)j * K + c, x);
+      *reinterpret_cast<float4*>(sK + j * (K + 4) + c) = make_float4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<float4*>(sK + j * (K + 4) + c + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    }
+    for (int idx = tid; idx < GR * (V / 8); idx += kGenThreads) {
+      const int j = idx / (V / 8), c = (idx - j * (V / 8)) * 8;
+      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (j0 + j < r.kv) load8(vt + (long)j * V + c, x);
+      *reinterpret_cast<float4*>(sV + j * V + c) = make_float4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<float4*>(sV + j * V + c + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    }
+    __syncthreads();
+    if (w0 >= ni) continue;  // warps past the block's rows only keep step
+    float d[kRowsPerWarp];
+#pragma unroll
+    for (int x = 0; x < kRowsPerWarp; ++x) d[x] = 0.f;
+    const float* krow = sK + lane * (K + 4);
+    for (int c = 0; c < K; c += 4) {
+      const float4 kx = *reinterpret_cast<const float4*>(krow + c);
+#pragma unroll
+      for (int x = 0; x < kRowsPerWarp; ++x) {
+        const float4 qx = *reinterpret_cast<const float4*>(sQ + (w0 + x) * K + c);
+        d[x] = fmaf(qx.x, kx.x, fmaf(qx.y, kx.y, fmaf(qx.z, kx.z, fmaf(qx.w, kx.w, d[x]))));
+      }
+    }
+    const int j = j0 + lane;
+    unsigned seen[kRowsPerWarp];
+    float pr[kRowsPerWarp];
+#pragma unroll
+    for (int x = 0; x < kRowsPerWarp; ++x) {
+      const int pos = r.ctx + row0 + w0 + x;
+      const bool vis = w0 + x < ni && j <= pos && j < r.kv && pos - j < win;
+      seen[x] = __ballot_sync(0xffffffffu, vis);
+      const float s = vis ? d[x] : -INFINITY;
+      float mx = s;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float mn = fmaxf(m[x], mx);
+      const float use = mn == -INFINITY ? 0.f : mn;
+      const float alpha = exp2f(m[x] - use);
+      pr[x] = vis ? exp2f(s - use) : 0.f;
+      float ps = pr[x];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
+      l[x] = l[x] * alpha + ps;
+      m[x] = mn;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[x][e] *= alpha;
+    }
+    // a masked key's value row may hold anything (NaN included): it is
+    // skipped, not multiplied by zero
+    for (int jj = 0; jj < GR; ++jj) {
+      float4 vx = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (lane * 4 < V) vx = *reinterpret_cast<const float4*>(sV + jj * V + lane * 4);
+#pragma unroll
+      for (int x = 0; x < kRowsPerWarp; ++x) {
+        const float pj = __shfl_sync(0xffffffffu, pr[x], jj);
+        if ((seen[x] >> jj) & 1u) {
+          acc[x][0] = fmaf(pj, vx.x, acc[x][0]);
+          acc[x][1] = fmaf(pj, vx.y, acc[x][1]);
+          acc[x][2] = fmaf(pj, vx.z, acc[x][2]);
+          acc[x][3] = fmaf(pj, vx.w, acc[x][3]);
+        }
+      }
+    }
+  }
+}
+
+// The finished rows of a block: o = acc / l and lse, the sink's weight in l.
+template <typename T>
+__device__ __forceinline__ void write_row(const AttnArgs& a, long token, int h, int lane, float m,
+                                          float l, const float (&acc)[4]) {
+  float mf = m, lt = l, f = 1.f;
+  if (a.sink) {
+    const float sk = a.sink[h] * kLog2e;
+    mf = fmaxf(m, sk);
+    f = m == -INFINITY ? 0.f : exp2f(m - mf);
+    lt = l * f + exp2f(sk - mf);
+  }
+  const float inv = lt > 0.f || lt != lt ? f / lt : 0.f;  // a row that sees nothing: 0
+  if (lane * 4 < a.V) {
+    T* o = static_cast<T*>(a.o) + ((long)token * a.HQ + h) * a.V + lane * 4;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = from_f32<T>(acc[e] * inv);
+  }
+  if (lane == 0 && a.lse) a.lse[token * a.HQ + h] = lt == 0.f ? -INFINITY : (mf + log2f(lt)) * kLn2;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kGenThreads) general_kernel(AttnArgs a, Pick pk, Parts parts) {
+  extern __shared__ __align__(16) float gen_shared[];
+  __shared__ FindScratch fs;
+  const int cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) parts.desc[cta].last_cta = -1;
+  Share sh;
+  if (!find_start<GR>(a.bt, a.window, a.HQ, pk, 1, cta, parts.n_cta, fs, sh)) return;
+  const long long x0 = sh.begin(cta), x1 = sh.begin(cta + 1);
+  Cursor c = cursor_at<GR>(a.bt, a.window, fs.req, fs.base, x0);
+  for (long long x = x0; x < x1;) {
+    const int ta = c.t, tb = (int)min((long long)c.n_tiles, ta + (x1 - x));
+    float m[kRowsPerWarp], l[kRowsPerWarp], acc[kRowsPerWarp][4];
+    gen_tiles<T>(a, c.r, c.h, c.b * GR, tile_lo(c.r, c.b), ta, tb, gen_shared, m, l, acc);
+    const int ni = min(GR, c.r.n - c.b * GR);
+    const bool whole = ta == 0 && tb == c.n_tiles;
+    const int slot = ta == 0 ? 1 : 0;
+    float* po = parts.o(cta, slot, a.V);
+    float* pm = parts.ml(cta, slot, a.V);
+#pragma unroll
+    for (int y = 0; y < kRowsPerWarp; ++y) {
+      const int row = warp * kRowsPerWarp + y;
+      if (row >= ni) continue;
+      if (whole) {
+        write_row<T>(a, c.r.t0 + c.b * GR + row, c.h, lane, m[y], l[y], acc[y]);
+      } else {
+        if (lane * 4 < a.V)
+          *reinterpret_cast<float4*>(po + (size_t)row * a.V + lane * 4) =
+              make_float4(acc[y][0], acc[y][1], acc[y][2], acc[y][3]);
+        if (lane == 0) {
+          pm[row * 2] = m[y];
+          pm[row * 2 + 1] = l[y];
+        }
+      }
+    }
+    if (!whole && slot == 1 && threadIdx.x == 0) {
+      PartDesc d;
+      d.req = c.r.i; d.h = c.h; d.b = c.b;
+      d.last_cta = sh.owner(x + c.n_tiles - 1);
+      parts.desc[cta] = d;
+    }
+    x += tb - ta;
+    if (x < x1) next_unit<GR>(a.bt, a.window, a.HQ, pk, c);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Joining the units that more than one CTA worked on: o = sum of the parts
+// weighted by 2^(m_part - m), over the sum of their l, in the order of the
+// CTAs (the same bits every time).  One warp a row; 4 channels a lane.
+// group > 0: a part's rows are the heads of one kv head, of a single token.
+constexpr int kJoinThreads = 256;
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, Parts parts, int group) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int cta = blockIdx.x;
+  if (cta == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < a.bt.N; i += kJoinThreads)
+      if (a.bt.rows(i) > a.max_new) record_status(a.status, WALL_ERR_INVALID_ARG);
+  const PartDesc d = parts.desc[cta];
+  if (d.last_cta < 0) return;
+  const int t0 = a.bt.start(d.req), n = a.bt.rows(d.req);
+  const int rows = group > 0 ? group : min(parts.rows, n - d.b * parts.rows);
+  const int np = d.last_cta - cta + 1;
+  const int stride = gridDim.y * (kJoinThreads / 32);
+  for (int row = blockIdx.y * (kJoinThreads / 32) + warp; row < rows; row += stride) {
+    float m = -INFINITY;
+    for (int s = lane; s < np; s += 32)
+      m = fmaxf(m, parts.ml(cta + s, s == 0 ? 1 : 0, a.V)[row * 2]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s0 = 0; s0 < np; s0 += 32) {
+      float f = 0.f;
+      if (s0 + lane < np) {
+        const float* ml = parts.ml(cta + s0 + lane, s0 + lane == 0 ? 1 : 0, a.V) + row * 2;
+        if (ml[0] != -INFINITY) {
+          f = exp2f(ml[0] - m);
+          l = fmaf(ml[1], f, l);
+        }
+      }
+      const int cnt = min(32, np - s0);
+      for (int j0 = 0; j0 < cnt; j0 += 8) {
+        float4 x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int s = s0 + min(j0 + j, cnt - 1);
+          x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (lane * 4 < a.V)
+            x[j] = *reinterpret_cast<const float4*>(parts.o(cta + s, s == 0 ? 1 : 0, a.V) +
+                                                    (size_t)row * a.V + lane * 4);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float fj = __shfl_sync(0xffffffffu, f, (j0 + j) & 31);
+          if (j0 + j < cnt && fj != 0.f) {
+            acc[0] = fmaf(x[j].x, fj, acc[0]);
+            acc[1] = fmaf(x[j].y, fj, acc[1]);
+            acc[2] = fmaf(x[j].z, fj, acc[2]);
+            acc[3] = fmaf(x[j].w, fj, acc[3]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (group > 0) write_row<T>(a, t0, d.h * group + row, lane, m, l, acc);
+    else write_row<T>(a, t0 + (long)d.b * parts.rows + row, d.h, lane, m, l, acc);
+  }
+}
+
+template <typename T>
+int join(const AttnArgs& a, const Parts& parts, int group, cudaStream_t stream) {
+  const int rows = group > 0 ? group : parts.rows;
+  join_kernel<T><<<dim3(parts.n_cta, ceil_div(rows, kJoinThreads / 32)), kJoinThreads, 0, stream>>>(
+      a, parts, group);
+  return cudaGetLastError() == cudaSuccess ? WALL_OK : WALL_ERR_CUDA;
+}
+
+template <typename T>
+int run_general(const AttnArgs& a, const Pick& pk, const Parts& parts, cudaStream_t stream) {
+  static bool attr[kMaxDevices] = {};
+  if (!set_max_smem_once(general_kernel<T>, (int)gen_smem(128, 128), attr)) return WALL_ERR_CUDA;
+  general_kernel<T><<<parts.n_cta, kGenThreads, gen_smem(a.K, a.V), stream>>>(a, pk, parts);
+  if (cudaGetLastError() != cudaSuccess) return WALL_ERR_CUDA;
+  return join<T>(a, parts, 0, stream);
+}
+
+size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct AttnWs {
+  size_t gen_desc, gen_data, total;
+};
+AttnWs attn_ws(int V) {
+  AttnWs w;
+  w.gen_desc = 0;
+  w.gen_data = al256(sizeof(PartDesc) * kGeneralCtas);
+  w.total = w.gen_data + al256(sizeof(float) * 2 * kGeneralCtas * (size_t)GR * (V + 2));
+  return w;
+}
+
+}  // namespace
+
+size_t paged_attn_ws(int dtype, int N, int T, int max_new, int H, int HQ, int K, int V) {
+  (void)dtype; (void)N; (void)T; (void)max_new; (void)H; (void)HQ; (void)K;
+  return attn_ws(V).total;
+}
+
+int paged_attn(const PagedAttnProblem& pb, void* ws, cudaStream_t stream) {
+  AttnArgs a;
+  a.q = pb.q; a.p = pb.p;
+  a.bt.cu = pb.cu; a.bt.kv = pb.kv; a.bt.N = pb.N; a.bt.T = pb.T;
+  a.table = pb.table; a.MP = pb.MP; a.NP = pb.NP; a.shift = pb.shift;
+  a.H = pb.H; a.HQ = pb.HQ; a.K = pb.K; a.V = pb.V;
+  a.kp = pb.k_pages; a.vp = pb.v_pages; a.rp = pb.r_pages;
+  a.sink = pb.sink;
+  a.scale_log2 = pb.scale * kLog2e;
+  a.window = pb.window;
+  a.max_new = pb.max_new;
+  a.o = pb.o; a.lse = pb.lse;
+  a.status = device_status();
+  const AttnWs w = attn_ws(pb.V);
+  char* base = static_cast<char*>(ws);
+  Parts gen;
+  gen.desc = reinterpret_cast<PartDesc*>(base + w.gen_desc);
+  gen.data = reinterpret_cast<float*>(base + w.gen_data);
+  gen.rows = GR;
+  gen.n_cta = kGeneralCtas;
+  const Pick all = {1, 0x7fffffff};
+  return pb.dtype == WALL_BF16 ? run_general<__nv_bfloat16>(a, all, gen, stream)
+                               : run_general<float>(a, all, gen, stream);
+}
+
+}  // namespace wall
