@@ -126,6 +126,11 @@ int attn_bwd_dq_tc(const AttnProblem& pb, const BwdArgs& a, const TcFwdWs& ws, i
 bool make_tile_map(CUtensorMap* m, const void* base, long rows, int heads, int dim,
                    int box_rows);
 
+// A pool [blocks, page_size, dim] bf16 (a block: one head of one page) viewed as
+// (dim, page_size, blocks); a box is 64 elements (128-byte swizzle) x box_rows
+// rows x box_blocks blocks.
+bool make_page_map(CUtensorMap* m, const void* base, long blocks, int page_size, int dim,
+                   int box_rows, int box_blocks);
 bool make_rows128_map(CUtensorMap* m, const void* base, long rows, int box_rows, int box_cols);
 bool make_cache_map(CUtensorMap* m, const void* base, int B, int T, int Tcap, int heads, int dim,
                     int box_rows);

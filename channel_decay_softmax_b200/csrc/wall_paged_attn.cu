@@ -305,22 +305,55 @@ int run_general(const AttnArgs& a, const Pick& pk, const Parts& parts, cudaStrea
 
 size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
-struct AttnWs {
-  size_t gen_desc, gen_data, total;
+// Which kernels a call runs.  Single-token rows stream through the decode
+// kernel where it covers the shape (else the general one); rows of more tokens
+// take the general kernel.
+struct Route {
+  bool decode;    // the decode kernel, for requests of one row
+  bool general;   // the general kernel
+  Pick rows;      // the requests it takes
 };
-AttnWs attn_ws(int V) {
+Route route_of(int dtype, int max_new, int H, int HQ, int K, int V) {
+  Route r;
+  r.decode = decode_rows_supported(dtype, H, HQ, K, V);
+  r.general = !r.decode || max_new > 1;
+  r.rows.n_min = r.decode ? 2 : 1;
+  r.rows.n_max = 0x7fffffff;
+  return r;
+}
+
+struct AttnWs {
+  size_t dec_desc, dec_data, gen_desc, gen_data, total;
+};
+AttnWs attn_ws(const Route& r, int H, int HQ, int V) {
   AttnWs w;
-  w.gen_desc = 0;
-  w.gen_data = al256(sizeof(PartDesc) * kGeneralCtas);
-  w.total = w.gen_data + al256(sizeof(float) * 2 * kGeneralCtas * (size_t)GR * (V + 2));
+  size_t off = 0;
+  auto take = [&](bool need, int ctas, int rows, size_t& desc, size_t& data) {
+    desc = off;
+    off += need ? al256(sizeof(PartDesc) * ctas) : 0;
+    data = off;
+    off += need ? al256(sizeof(float) * 2 * ctas * Parts::stride_of(rows, V)) : 0;
+  };
+  take(r.decode, kSms, HQ / H, w.dec_desc, w.dec_data);
+  take(r.general, kGeneralCtas, GR, w.gen_desc, w.gen_data);
+  w.total = off;
   return w;
+}
+
+Parts parts_at(void* ws, size_t desc, size_t data, int rows, int ctas) {
+  Parts p;
+  p.desc = reinterpret_cast<PartDesc*>(static_cast<char*>(ws) + desc);
+  p.data = reinterpret_cast<float*>(static_cast<char*>(ws) + data);
+  p.rows = rows;
+  p.n_cta = ctas;
+  return p;
 }
 
 }  // namespace
 
 size_t paged_attn_ws(int dtype, int N, int T, int max_new, int H, int HQ, int K, int V) {
-  (void)dtype; (void)N; (void)T; (void)max_new; (void)H; (void)HQ; (void)K;
-  return attn_ws(V).total;
+  (void)N; (void)T;
+  return attn_ws(route_of(dtype, max_new, H, HQ, K, V), H, HQ, V).total;
 }
 
 int paged_attn(const PagedAttnProblem& pb, void* ws, cudaStream_t stream) {
@@ -336,16 +369,22 @@ int paged_attn(const PagedAttnProblem& pb, void* ws, cudaStream_t stream) {
   a.max_new = pb.max_new;
   a.o = pb.o; a.lse = pb.lse;
   a.status = device_status();
-  const AttnWs w = attn_ws(pb.V);
-  char* base = static_cast<char*>(ws);
-  Parts gen;
-  gen.desc = reinterpret_cast<PartDesc*>(base + w.gen_desc);
-  gen.data = reinterpret_cast<float*>(base + w.gen_data);
-  gen.rows = GR;
-  gen.n_cta = kGeneralCtas;
-  const Pick all = {1, 0x7fffffff};
-  return pb.dtype == WALL_BF16 ? run_general<__nv_bfloat16>(a, all, gen, stream)
-                               : run_general<float>(a, all, gen, stream);
+  const Route r = route_of(pb.dtype, pb.max_new, pb.H, pb.HQ, pb.K, pb.V);
+  const AttnWs w = attn_ws(r, pb.H, pb.HQ, pb.V);
+  if (r.decode) {
+    const int G = pb.HQ / pb.H;
+    const Parts p = parts_at(ws, w.dec_desc, w.dec_data, G, kSms);
+    int rc = decode_rows(a, p, stream);
+    if (rc) return rc;
+    rc = join<__nv_bfloat16>(a, p, G, stream);
+    if (rc) return rc;
+  }
+  if (r.general) {
+    const Parts p = parts_at(ws, w.gen_desc, w.gen_data, GR, kGeneralCtas);
+    return pb.dtype == WALL_BF16 ? run_general<__nv_bfloat16>(a, r.rows, p, stream)
+                                 : run_general<float>(a, r.rows, p, stream);
+  }
+  return WALL_OK;
 }
 
 }  // namespace wall

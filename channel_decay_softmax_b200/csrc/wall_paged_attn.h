@@ -39,7 +39,11 @@ struct Parts {
   float* data;
   int rows;
   int n_cta;
-  __host__ __device__ size_t stride(int V) const { return (size_t)rows * (V + 2); }
+  // floats of one part: whole 16-byte vectors, whatever the number of rows
+  __host__ __device__ static size_t stride_of(int rows, int V) {
+    return ((size_t)rows * (V + 2) + 3) & ~size_t(3);
+  }
+  __device__ __forceinline__ size_t stride(int V) const { return stride_of(rows, V); }
   __device__ __forceinline__ float* o(int cta, int slot, int V) const {
     return data + ((size_t)cta * 2 + slot) * stride(V);
   }
@@ -47,6 +51,10 @@ struct Parts {
     return o(cta, slot, V) + (size_t)rows * V;
   }
 };
+
+// single-token rows (wall_paged_decode.cu): Parts of HQ / H rows, kSms CTAs
+bool decode_rows_supported(int dtype, int H, int HQ, int K, int V);
+int decode_rows(const AttnArgs& a, const Parts& parts, cudaStream_t stream);
 
 }  // namespace paged
 }  // namespace wall

@@ -60,6 +60,20 @@ bool make_cache_map(CUtensorMap* m, const void* base, int B, int T, int Tcap, in
   return r == CUDA_SUCCESS;
 }
 
+bool make_page_map(CUtensorMap* m, const void* base, long blocks, int page_size, int dim,
+                   int box_rows, int box_blocks) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || blocks <= 0 || dim % 64 != 0) return false;
+  cuuint64_t gdim[3] = {(cuuint64_t)dim, (cuuint64_t)page_size, (cuuint64_t)blocks};
+  cuuint64_t gstride[2] = {(cuuint64_t)dim * 2, (cuuint64_t)dim * page_size * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_blocks};
+  cuuint32_t estride[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), gdim, gstride,
+                  box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // A [rows, 128] bf16 array of stored 128 x 128 tiles viewed as the 2-D tensor
 // (128, rows).  Loads: one box is 64 columns (128 B, 128-byte swizzle) x
 // box_rows rows.  Stores: 32 columns (64 B, 64-byte swizzle) x box_rows.
