@@ -221,6 +221,36 @@ __global__ void __launch_bounds__(kGenThreads) general_kernel(AttnArgs a, Pick p
   }
 }
 
+// The units that the tensor-core kernel flagged, again and whole: a grid over
+// (request's 128-row block, head, 32 rows of it), whose CTAs read one word and
+// leave when nothing is flagged.
+template <typename T>
+__global__ void __launch_bounds__(kGenThreads) flagged_kernel(AttnArgs a, UnitFlags flags) {
+  extern __shared__ __align__(16) float gen_shared[];
+  if (*flags.any(a.HQ) == 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int at = 0;  // (block, head, quarter) items before the request
+  for (int i = 0; i < a.bt.N; ++i) {
+    const int n = a.bt.rows(i);
+    if (n < 2) continue;
+    const Request r = request_of<GR>(a.bt, i, a.window);
+    const int items = r.nb * a.HQ;  // 32-row blocks of every head
+    const int first = ((int)blockIdx.x - at % (int)gridDim.x + (int)gridDim.x) % (int)gridDim.x;
+    for (int x = first; x < items; x += gridDim.x) {
+      const int b = x / a.HQ, h = x - b * a.HQ;
+      if (*flags.at(r, b * GR / kChunkRows, h, a.HQ) == 0) continue;
+      float m[kRowsPerWarp], l[kRowsPerWarp], acc[kRowsPerWarp][4];
+      gen_tiles<T>(a, r, h, b * GR, tile_lo(r, b), 0, unit_tiles(r, b), gen_shared, m, l, acc);
+#pragma unroll
+      for (int y = 0; y < kRowsPerWarp; ++y) {
+        const int row = b * GR + warp * kRowsPerWarp + y;
+        if (row < n) write_row<T>(a, r.t0 + row, h, lane, m[y], l[y], acc[y]);
+      }
+    }
+    at = (at + items) % (int)gridDim.x;
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Joining the units that more than one CTA worked on: o = sum of the parts
 // weighted by 2^(m_part - m), over the sum of their l, in the order of the
@@ -305,27 +335,37 @@ int run_general(const AttnArgs& a, const Pick& pk, const Parts& parts, cudaStrea
 
 size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Which kernels a call runs.  Single-token rows stream through the decode
-// kernel where it covers the shape (else the general one); rows of more tokens
-// take the general kernel.
+template <typename T>
+int run_flagged(const AttnArgs& a, const UnitFlags& flags, cudaStream_t stream) {
+  static bool attr[kMaxDevices] = {};
+  if (!set_max_smem_once(flagged_kernel<T>, (int)gen_smem(128, 128), attr)) return WALL_ERR_CUDA;
+  flagged_kernel<T><<<kGeneralCtas, kGenThreads, gen_smem(a.K, a.V), stream>>>(a, flags);
+  return cudaGetLastError() == cudaSuccess ? WALL_OK : WALL_ERR_CUDA;
+}
+
+// Which kernels a call runs: single-token rows stream through the decode
+// kernel and rows of requests of more through the tensor cores where those
+// cover the shape; the general kernel takes what is left.
 struct Route {
   bool decode;    // the decode kernel, for requests of one row
+  bool chunk;     // the tensor-core kernel, for requests of two or more
   bool general;   // the general kernel
   Pick rows;      // the requests it takes
 };
 Route route_of(int dtype, int max_new, int H, int HQ, int K, int V) {
   Route r;
   r.decode = decode_rows_supported(dtype, H, HQ, K, V);
-  r.general = !r.decode || max_new > 1;
+  r.chunk = max_new > 1 && chunk_rows_supported(dtype, K, V);
   r.rows.n_min = r.decode ? 2 : 1;
-  r.rows.n_max = 0x7fffffff;
+  r.rows.n_max = r.chunk ? 1 : 0x7fffffff;
+  r.general = !r.decode || (max_new > 1 && !r.chunk);
   return r;
 }
 
 struct AttnWs {
-  size_t dec_desc, dec_data, gen_desc, gen_data, total;
+  size_t dec_desc, dec_data, chunk_desc, chunk_data, qh, flags, gen_desc, gen_data, total;
 };
-AttnWs attn_ws(const Route& r, int H, int HQ, int V) {
+AttnWs attn_ws(const Route& r, int N, int T, int H, int HQ, int K, int V) {
   AttnWs w;
   size_t off = 0;
   auto take = [&](bool need, int ctas, int rows, size_t& desc, size_t& data) {
@@ -335,6 +375,11 @@ AttnWs attn_ws(const Route& r, int H, int HQ, int V) {
     off += need ? al256(sizeof(float) * 2 * ctas * Parts::stride_of(rows, V)) : 0;
   };
   take(r.decode, kSms, HQ / H, w.dec_desc, w.dec_data);
+  take(r.chunk, kSms, kChunkRows, w.chunk_desc, w.chunk_data);
+  w.qh = off;
+  off += r.chunk ? al256((size_t)2 * T * HQ * K) : 0;
+  w.flags = off;
+  off += r.chunk ? al256(sizeof(int) * (size_t)UnitFlags::count(N, T, HQ)) : 0;
   take(r.general, kGeneralCtas, GR, w.gen_desc, w.gen_data);
   w.total = off;
   return w;
@@ -352,8 +397,7 @@ Parts parts_at(void* ws, size_t desc, size_t data, int rows, int ctas) {
 }  // namespace
 
 size_t paged_attn_ws(int dtype, int N, int T, int max_new, int H, int HQ, int K, int V) {
-  (void)N; (void)T;
-  return attn_ws(route_of(dtype, max_new, H, HQ, K, V), H, HQ, V).total;
+  return attn_ws(route_of(dtype, max_new, H, HQ, K, V), N, T, H, HQ, K, V).total;
 }
 
 int paged_attn(const PagedAttnProblem& pb, void* ws, cudaStream_t stream) {
@@ -370,13 +414,25 @@ int paged_attn(const PagedAttnProblem& pb, void* ws, cudaStream_t stream) {
   a.o = pb.o; a.lse = pb.lse;
   a.status = device_status();
   const Route r = route_of(pb.dtype, pb.max_new, pb.H, pb.HQ, pb.K, pb.V);
-  const AttnWs w = attn_ws(r, pb.H, pb.HQ, pb.V);
+  const AttnWs w = attn_ws(r, pb.N, pb.T, pb.H, pb.HQ, pb.K, pb.V);
   if (r.decode) {
     const int G = pb.HQ / pb.H;
     const Parts p = parts_at(ws, w.dec_desc, w.dec_data, G, kSms);
     int rc = decode_rows(a, p, stream);
     if (rc) return rc;
     rc = join<__nv_bfloat16>(a, p, G, stream);
+    if (rc) return rc;
+  }
+  if (r.chunk) {
+    const Parts p = parts_at(ws, w.chunk_desc, w.chunk_data, kChunkRows, kSms);
+    UnitFlags flags;
+    flags.f = reinterpret_cast<int*>(static_cast<char*>(ws) + w.flags);
+    flags.places_n = (int)UnitFlags::places(pb.N, pb.T);
+    int rc = chunk_rows(a, p, flags, static_cast<char*>(ws) + w.qh, stream);
+    if (rc) return rc;
+    rc = join<__nv_bfloat16>(a, p, 0, stream);
+    if (rc) return rc;
+    rc = run_flagged<__nv_bfloat16>(a, flags, stream);
     if (rc) return rc;
   }
   if (r.general) {

@@ -12,6 +12,7 @@ namespace paged {
 constexpr int kSms = 148;
 constexpr int kGeneralCtas = kSms * 4;
 constexpr int kGeneralRows = 32;  // query rows of a general unit, keys of a tile
+constexpr int kChunkRows = 128;   // the same of the tensor-core kernel
 
 struct AttnArgs {
   const void* q;        // [T, HQ, K]
@@ -51,6 +52,32 @@ struct Parts {
     return o(cta, slot, V) + (size_t)rows * V;
   }
 };
+
+// The tensor-core kernel's units that the general kernel computes again: a word
+// for each (128-row block, head), cleared by every call, and one more that says
+// whether any is set.  Block b of request i has place t0 / 128 + i + b, which
+// no two share (a request of n rows starting at t0 ends before place
+// (t0 + n) / 128 + i + 1).
+struct UnitFlags {
+  int* f;
+  __host__ __device__ static long places(int N, int T) { return (long)T / kChunkRows + N; }
+  __host__ __device__ static long count(int N, int T, int HQ) { return places(N, T) * HQ + 1; }
+  int places_n;
+  __device__ __forceinline__ int* any(int HQ) const { return f + (long)places_n * HQ; }
+  __device__ __forceinline__ int* at(const Request& r, int b, int h, int HQ) const {
+    return f + ((long)r.t0 / kChunkRows + r.i + b) * HQ + h;
+  }
+  __device__ __forceinline__ void set(const Request& r, int b, int h, int HQ) const {
+    set_flag(at(r, b, h, HQ));
+    set_flag(any(HQ));
+  }
+};
+
+// rows of requests of two or more (wall_paged_chunk_sm100.cu): Parts of
+// kChunkRows rows, kSms CTAs; qh: bf16 [T, HQ, K] of scratch
+bool chunk_rows_supported(int dtype, int K, int V);
+int chunk_rows(const AttnArgs& a, const Parts& parts, const UnitFlags& flags, void* qh,
+               cudaStream_t stream);
 
 // single-token rows (wall_paged_decode.cu): Parts of HQ / H rows, kSms CTAs
 bool decode_rows_supported(int dtype, int H, int HQ, int K, int V);

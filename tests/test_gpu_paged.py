@@ -445,6 +445,20 @@ def test_attn_long_context_and_many_splits():
     _attn_case(1, 1, 64, 64, 32, BF, [1 + i % 3 for i in range(400)], [i % 70 for i in range(400)])
 
 
+@pytest.mark.parametrize("K,window", [(128, 130), (64, 0), (128, 0)])
+def test_attn_many_units(K, window):
+    """More units than CTAs, of one to three tiles each: every CTA's pipeline
+    runs across units, with and without whole ones in its share."""
+    new = [2 + (37 * i) % 140 for i in range(120)]
+    _attn_case(2, 1, K, K, 64, BF, new, [(53 * i) % 200 for i in range(120)], window=window,
+               poison=True)
+
+
+def test_attn_long_windowed_prompts():
+    """Many tiles and many units a CTA, two partly masked tiles in each."""
+    _attn_case(16, 2, 128, 128, 64, BF, [520, 390], [700, 30], window=300, sink=True)
+
+
 @pytest.mark.parametrize("K,dt", [(128, BF), (64, BF), (64, F32)])
 @pytest.mark.parametrize("decay", [1.2, 2.0])
 def test_attn_strong_decay(K, dt, decay):
