@@ -64,11 +64,12 @@ struct UnitFlags {
   __host__ __device__ static long count(int N, int T, int HQ) { return places(N, T) * HQ + 1; }
   int places_n;
   __device__ __forceinline__ int* any(int HQ) const { return f + (long)places_n * HQ; }
-  __device__ __forceinline__ int* at(const Request& r, int b, int h, int HQ) const {
-    return f + ((long)r.t0 / kChunkRows + r.i + b) * HQ + h;
+  __device__ __forceinline__ long place(const Request& r, int b) const {
+    return (long)r.t0 / kChunkRows + r.i + b;
   }
-  __device__ __forceinline__ void set(const Request& r, int b, int h, int HQ) const {
-    set_flag(at(r, b, h, HQ));
+  __device__ __forceinline__ int* at(long place, int h, int HQ) const { return f + place * HQ + h; }
+  __device__ __forceinline__ void set(long place, int h, int HQ) const {
+    set_flag(at(place, h, HQ));
     set_flag(any(HQ));
   }
 };

@@ -21,8 +21,10 @@
 // spread over all SMs and are joined afterwards.
 //
 // 12 warps (3 per SM sub-partition, 168 registers each):
-//   warp 0      TMA, one thread: the key ring (3 stages, with the pages'
-//               anchors), the value ring (2 stages), the units' Qh
+//   warp 0      walks the share's units, lays each one's figures into a ring in
+//               shared memory for the other roles, and issues all TMA copies:
+//               the key ring (3 stages, with the pages' anchors), the value
+//               ring (2 stages), the units' Qh
 //   warp 1      TMEM owner and MMA issuer (one thread)
 //   warps 2-3   key rescale in place; partly masked tiles: value rows past the
 //               request's end zeroed (pages end inside tiles; what they hold
@@ -52,6 +54,29 @@ constexpr int kVS = 2;                    // value stages
 constexpr float kRescaleThreshold = 8.f;  // log2 units: lazy O rescale
 constexpr float kRescaleBound = 256.f;    // 2^kRescaleThreshold
 
+// A CTA's piece of one unit, as every role reads it.
+struct Segment {
+  int t0, ni;       // first query row among the packed ones, rows
+  int pos0;         // position of the first row (far below 0 where the request sees nothing)
+  int j0;           // first key of its first tile
+  int cnt;          // tiles
+  int fa, fb;       // tiles [fa, fb) are seen whole by every row
+  int kv;           // keys of the request (0 where it sees nothing)
+  int from;         // first key that any row sees
+  int h;
+  int req;
+  int page_i;       // the page whose anchor the unit's queries are taken against, or -1
+  int place;        // of its flag
+  int whole;        // the unit lies in this CTA alone
+  int slot;         // else its part's slot
+  int last_cta;     // and the CTA that ends it
+};
+static_assert(sizeof(Segment) == 64, "four 16-byte words");
+// Segments in flight: warp 0 writes the entry of segment s + 8 when its first
+// key tile g is issued, behind S(g - 3), hence behind PV(g - 5), whose segment
+// is s + 3 at least and began behind the epilogue of s + 2.
+constexpr int kSegs = 8;
+
 template <int KD>
 struct Smem {
   static constexpr int kT = BN * KD * 2;           // one 128-row bf16 tile
@@ -61,8 +86,9 @@ struct Smem {
   static constexpr int oV = oK + kKS * kT;         // kVS stages
   static constexpr int oR = oV + kVS * kT;         // int[kKS][kRows][KD] anchors
   static constexpr int oX = oR + kKS * kRows * KD * 4;  // float[2][2 groups][2][BM]: m, l
-  static constexpr int oBar = oX + 2 * 2 * 2 * BM * 4;
-  static constexpr int kBars = 26;
+  static constexpr int oSeg = oX + 2 * 2 * 2 * BM * 4;  // Segment[kSegs]
+  static constexpr int oBar = oSeg + kSegs * 64;
+  static constexpr int kBars = 26 + kSegs;
   static constexpr int oMisc = oBar + kBars * 8;   // TMEM base, abort flag
   static constexpr int kBytes = oMisc + 16;
   static constexpr int kAlloc = kBytes + 1024;     // slack for 1 KB alignment
@@ -84,7 +110,8 @@ enum Bar {
   B_XCHG = B_PVDONE + 2,        // exchange of m, l between the groups (8 warps)
   B_OEMPTY,                     // both O accumulators read (8 warps)
   B_MMADONE,
-  kNumBars,
+  B_SEG,                        // + ring entry: a segment's figures are there
+  kNumBars = B_SEG + kSegs,
 };
 static_assert(kNumBars <= Smem<128>::kBars, "barrier slots");
 
@@ -119,29 +146,6 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
   return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
 }
 
-// The CTA's run of tiles, unit by unit.
-struct Segment {
-  int t0;         // first query row of the unit among the packed ones
-  int ni;         // its rows
-  int pos0;       // position of the first
-  int lo;         // first tile
-  int ta, tb;     // the segment's tiles, counted from lo
-};
-__device__ __forceinline__ Segment segment_of(const Cursor& c, long long left) {
-  Segment s;
-  s.t0 = c.r.t0 + c.b * BM;
-  s.ni = min(BM, c.r.n - c.b * BM);
-  s.pos0 = c.r.ctx + c.b * BM;
-  s.lo = tile_lo(c.r, c.b);
-  s.ta = c.t;
-  s.tb = (int)min((long long)c.n_tiles, c.t + left);
-  return s;
-}
-// Whether every row of the unit sees all of the tile that begins at j0.
-__device__ __forceinline__ bool sees_all(const Segment& s, bool dead, int j0, int win) {
-  return !dead && j0 + BN - 1 <= s.pos0 && s.pos0 + s.ni - 1 - j0 < win;
-}
-
 template <int KD>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -152,20 +156,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int V = KD;
   extern __shared__ uint8_t smem_raw[];
   __shared__ FindScratch fs;
-  __shared__ Cursor s_cur[8];  // the softmax warps' places (their registers are full)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   float* sX = reinterpret_cast<float*>(smem + Lay::oX);
+  Segment* segs = reinterpret_cast<Segment*>(smem + Lay::oSeg);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::oBar);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Lay::oMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::oMisc + 4);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cta = blockIdx.x;
-  const int HQ = a.HQ;
-  const int win = a.window > 0 ? a.window : 0x7fffffff;
-  const Pick pk = {2, 0x7fffffff};
 
   if (threadIdx.x == 0) {
     parts.desc[cta].last_cta = -1;
@@ -189,14 +190,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(B_XCHG), 8);
     mbar_init(bar(B_OEMPTY), 8);
     mbar_init(bar(B_MMADONE), 1);
+    for (int s = 0; s < kSegs; ++s) mbar_init(bar(B_SEG + s), 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
   Share sh;
-  if (!find_start<BM>(a.bt, a.window, HQ, pk, 2, cta, parts.n_cta, fs, sh)) return;
-  const long long x0 = sh.begin(cta), x1 = sh.begin(cta + 1);
-  const int n_tiles = (int)(x1 - x0);  // of this CTA
-  Cursor c = cursor_at<BM>(a.bt, a.window, fs.req, fs.base, x0);
+  if (!find_start<BM>(a.bt, a.window, a.HQ, {2, 0x7fffffff}, 2, cta, parts.n_cta, fs, sh)) return;
+  const int n_tiles = (int)(sh.begin(cta + 1) - sh.begin(cta));  // of this CTA
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_holder), 512);
     tmem_relinquish();
@@ -205,132 +205,182 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const int PS = 1 << a.shift;
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA
-    // One thread issues every copy, in the order in which the MMAs free their
-    // places: S(0) S(1) PV(0) S(2) PV(1) S(3) ... complete in that order, so
-    // key tile g (behind S(g - 3)), then value tile g - 2 (behind PV(g - 4))
-    // never waits past a copy that could go.  A unit's Qh goes out once the
-    // last S of the unit before has read its rows, two tiles into the unit.
+    // Copies go out in the order in which the MMAs free their places: S(0)
+    // S(1) PV(0) S(2) PV(1) S(3) ... complete in that order, so key tile g
+    // (behind S(g - 3)), then value tile g - 2 (behind PV(g - 4)) never waits
+    // past a copy that could go.  A unit's Qh goes out once the last S of the
+    // unit before has read its rows, two tiles into the unit.  The lanes hold
+    // the next 32 entries of the block table and issue a tile's boxes side by
+    // side.
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
       tma_prefetch_desc(&tm_q);
-      Cursor cv = c;                    // of value tile (and unit) g - 2
-      int seg_v = 0, k_out = 0, v_out = 0, q_out = 0;
-      uint32_t raw = 0, raw_next = 0;   // per value stage: its last tile is a partly masked one;
-                                        // parity of the next one's B_VRAW phase
-      long long xk = x0, xv = x0;       // where the current units' segments begin
-      Segment sk = segment_of(c, x1 - xk), sv = sk;
-      int tk = sk.ta, tv = sv.ta;
-      auto load_q = [&]() {
-        mbar_expect_tx(bar(B_QFULL), Lay::kT);
-        for (int bx = 0; bx < KD / 64; ++bx)
-          tma_load_3d(sbase + Lay::oQ + bx * (BM * 128), &tm_q, bar(B_QFULL), bx * 64, cv.h, sv.t0);
-        ++q_out;
-      };
-      // the pages that hold tile t's keys into stage st of the key or value ring
-      auto load_tile = [&](auto keys_tag, const Cursor& cc, const Segment& s, int t, int st,
-                           uint32_t full) {
-        constexpr bool keys = decltype(keys_tag)::value;
-        const CUtensorMap* tm = keys ? &tm_k : &tm_v;
-        const uint32_t dst = sbase + (keys ? Lay::oK : Lay::oV) + st * Lay::kT;
-        const int j0 = (s.lo + t) * BN;
-        const int nk = cc.r.dead ? 0 : min(BN, cc.r.kv - j0);
-        const int np = (nk + PS - 1) >> a.shift;
-        const int heads = keys ? HQ : a.H, hd = keys ? cc.h : cc.h / (HQ / a.H);
-        mbar_expect_tx(full, np * (PS * KD * 2 + (keys ? KD * 4 : 0)));
-        for (int y = 0; y < np; ++y) {
-          const int slot = (j0 >> a.shift) + y;
-          const int page = slot < a.MP ? page_of(a.table, (long)cc.r.i * a.MP, slot, a.NP) : -1;
-          // none: read past the pool's end, where the copy gives zeros
-          // (expected only of pages wholly before the window)
-          if (page < 0 && j0 + ((y + 1) << a.shift) > max(0, s.pos0 - win + 1))
-            record_status(a.status, WALL_ERR_INVALID_ARG);
-          const int z = page >= 0 ? page * heads + hd : a.NP * heads;
-          for (int bx = 0; bx < KD / 64; ++bx)
-            tma_load_3d(dst + bx * (BN * 128) + y * PS * 128, tm, full, bx * 64, 0, z);
-          if constexpr (keys)
-            bulk_load(sbase + Lay::oR + (st * Lay::kRows + y) * KD * 4,
-                      a.rp + ((long)max(page, 0) * HQ + cc.h) * KD, KD * 4, full);
-        }
-      };
-      load_q();
-      for (int g = 0; g < n_tiles + 2; ++g) {
-        if (g >= 2 && tv == sv.ta && seg_v > 0) {
-          if (!wait_bar(bar(B_QEMPTY), (seg_v - 1) & 1, a.status, abort_flag)) break;
-          load_q();
-        }
-        if (g < n_tiles) {
-          const int st = g % kKS;
-          if (g >= kKS && !wait_bar(bar(B_KEMPTY + st), (g / kKS - 1) & 1, a.status, abort_flag))
-            break;
-          load_tile(std::true_type{}, c, sk, tk, st, bar(B_KFULL + st));
-          ++k_out;
-          if (++tk == sk.tb && g + 1 < n_tiles) {
-            xk += sk.tb - sk.ta;
-            next_unit<BM>(a.bt, a.window, HQ, pk, c);
-            sk = segment_of(c, x1 - xk);
-            tk = sk.ta;
-          }
-        }
-        if (g >= 2) {
-          const int gv = g - 2, st = gv % kVS;
-          if (gv >= kVS && !wait_bar(bar(B_VEMPTY + st), (gv / kVS - 1) & 1, a.status, abort_flag))
-            break;
-          // a partly masked tile goes to the rescale warps first, which then
-          // make the two arrivals on B_VFULL
-          const bool part = !sees_all(sv, cv.r.dead, (sv.lo + tv) * BN, win);
-          if (part) {
-            raw |= 1u << st;
-            raw_next ^= 1u << st;
-          } else {
-            raw &= ~(1u << st);
-            mbar_arrive(bar(B_VFULL + st));
-          }
-          load_tile(std::false_type{}, cv, sv, tv, st, bar((part ? B_VRAW : B_VFULL) + st));
-          ++v_out;
-          if (++tv == sv.tb && gv + 1 < n_tiles) {
-            xv += sv.tb - sv.ta;
-            next_unit<BM>(a.bt, a.window, HQ, pk, cv);
-            sv = segment_of(cv, x1 - xv);
-            tv = sv.ta;
-            ++seg_v;
-          }
-        }
-      }
-      // no copy may still be landing in this CTA's shared memory at exit
-      for (int t = max(0, k_out - kKS); t < k_out; ++t)
-        mbar_wait(bar(B_KFULL + t % kKS), (t / kKS) & 1, a.status);
-      for (int t = max(0, v_out - kVS); t < v_out; ++t) {
-        const int st = t % kVS;
-        if ((raw >> st) & 1u) mbar_wait(bar(B_VRAW + st), ((raw_next >> st) & 1u) ^ 1u, a.status);
-        else mbar_wait(bar(B_VFULL + st), (t / kVS) & 1, a.status);
-      }
-      mbar_wait(bar(B_QFULL), (q_out - 1) & 1, a.status);
     }
+    constexpr int kBoxes = KD / 64;
+    const int win = a.window > 0 ? a.window : 0x7fffffff;
+    const int PS = 1 << a.shift;
+    // 32 entries of a request's table row from `slot` on
+    auto table_at = [&](int req, int slot) {
+      return slot + lane < a.MP ? page_of(a.table, (long)req * a.MP, slot + lane, a.NP) : -1;
+    };
+    Cursor c = cursor_at<BM>(a.bt, a.window, fs.req, fs.base, sh.begin(cta));
+    int slot_k = 0, ids_k = 0, seg_k = -1;
+    // the figures of the cursor's unit, of which this CTA has `left` tiles at
+    // most, into the ring; returns its number of tiles
+    auto open_segment = [&](int left) {
+      const int lo = tile_lo(c.r, c.b);
+      Segment s;
+      s.t0 = c.r.t0 + c.b * BM;
+      s.ni = min(BM, c.r.n - c.b * BM);
+      s.pos0 = c.r.dead ? -(1 << 29) : c.r.ctx + c.b * BM;
+      s.j0 = (lo + c.t) * BN;
+      s.cnt = min(c.n_tiles - c.t, left);
+      // seen whole: the first row sees its last key, the last row its first
+      s.fa = c.r.dead ? 0 : max(0, (max(s.pos0 + s.ni - win, 0) - s.j0 + BN - 1) >> 7);
+      s.fb = c.r.dead ? 0 : max(0, (s.pos0 + 1 - s.j0) >> 7);
+      s.kv = c.r.dead ? 0 : c.r.kv;
+      s.from = c.r.dead ? 0 : max(0, s.pos0 - win + 1);
+      s.h = c.h;
+      s.req = c.r.i;
+      slot_k = s.j0 >> a.shift;
+      ids_k = c.r.dead ? -1 : table_at(s.req, slot_k);
+      const int slot_i = s.pos0 >> a.shift;  // (one entry, the same for every lane)
+      s.page_i = !c.r.dead && slot_i < a.MP ? page_of(a.table, (long)s.req * a.MP, slot_i, a.NP) : -1;
+      s.place = (int)flags.place(c.r, c.b);
+      s.whole = c.t == 0 && s.cnt == c.n_tiles;
+      s.slot = c.t == 0 ? 1 : 0;
+      s.last_cta = -1;
+      if (c.t == 0 && !s.whole) s.last_cta = sh.owner(sh.begin(cta) + (n_tiles - left) + c.n_tiles - 1);
+      ++seg_k;
+      if (lane == 0) {
+        segs[seg_k % kSegs] = s;
+        mbar_arrive(bar(B_SEG + seg_k % kSegs));
+        if (s.last_cta >= 0) {
+          PartDesc d;
+          d.req = s.req; d.h = s.h; d.b = c.b; d.last_cta = s.last_cta;
+          parts.desc[cta] = d;
+        }
+      }
+      __syncwarp();
+      return s.cnt;
+    };
+    // the pages that hold the keys from j0 on into a stage of a ring
+    auto load_tile = [&](auto keys_tag, const Segment& s, int j0, int st, uint32_t full, int& slot0,
+                         int& ids) {
+      constexpr bool keys = decltype(keys_tag)::value;
+      const CUtensorMap* tm = keys ? &tm_k : &tm_v;
+      const uint32_t dst = sbase + (keys ? Lay::oK : Lay::oV) + st * Lay::kT;
+      const int np = (max(0, min(BN, s.kv - j0)) + PS - 1) >> a.shift;
+      const int slot = j0 >> a.shift;
+      if (slot + (BN >> a.shift) > slot0 + 32) {
+        slot0 = slot;
+        ids = table_at(s.req, slot);
+      }
+      if (lane == 0) mbar_expect_tx(full, np * (PS * KD * 2 + (keys ? KD * 4 : 0)));
+      const int y = lane / kBoxes, bx = lane % kBoxes;  // page of the tile, box of the page
+      const int page = __shfl_sync(0xffffffffu, ids, slot - slot0 + y);
+      if (y < np) {
+        const int heads = keys ? a.HQ : a.H, hd = keys ? s.h : s.h / (a.HQ / a.H);
+        // none: read past the pool's end, where the copy gives zeros (expected
+        // only of pages wholly before the window)
+        if (page < 0 && j0 + ((y + 1) << a.shift) > s.from)
+          record_status(a.status, WALL_ERR_INVALID_ARG);
+        tma_load_3d(dst + bx * (BN * 128) + y * PS * 128, tm, full, bx * 64, 0,
+                    page >= 0 ? page * heads + hd : a.NP * heads);
+        if (keys && bx == 0)
+          bulk_load(sbase + Lay::oR + (st * Lay::kRows + y) * KD * 4,
+                    a.rp + ((long)max(page, 0) * a.HQ + s.h) * KD, KD * 4, full);
+      }
+      __syncwarp();
+    };
+    auto waits = [&](int b, int parity) {
+      return __all_sync(0xffffffffu, wait_bar(bar(b), parity & 1, a.status, abort_flag));
+    };
+    int left_k = 0, y_k = 0;            // key tiles left in the walker's segment; the next one
+    int left_v = 0, y_v = 0, seg_v = -1;
+    int slot_v = 0, ids_v = 0;
+    int k_out = 0, v_out = 0, q_out = 0;
+    uint32_t raw = 0, raw_next = 0;     // per value stage: its last tile is a partly masked one;
+                                        // parity of the next one's B_VRAW phase
+    for (int g = 0; g < n_tiles + 2; ++g) {
+      if (g >= 2 && left_v == 0) {      // value tile g - 2 opens a segment: its queries
+        const Segment& s = segs[++seg_v % kSegs];
+        left_v = s.cnt;
+        y_v = 0;
+        slot_v = s.j0 >> a.shift;
+        ids_v = s.kv > 0 ? table_at(s.req, slot_v) : -1;
+        if (seg_v > 0 && !waits(B_QEMPTY, seg_v - 1)) break;
+        if (lane == 0) mbar_expect_tx(bar(B_QFULL), Lay::kT);
+        __syncwarp();
+        if (lane < kBoxes)
+          tma_load_3d(sbase + Lay::oQ + lane * (BM * 128), &tm_q, bar(B_QFULL), lane * 64, s.h, s.t0);
+        ++q_out;
+      }
+      if (g < n_tiles) {
+        if (left_k == 0) {
+          if (g > 0) next_unit<BM>(a.bt, a.window, a.HQ, {2, 0x7fffffff}, c);
+          left_k = open_segment(n_tiles - g);
+          y_k = 0;
+        }
+        const int st = g % kKS;
+        if (g >= kKS && !waits(B_KEMPTY + st, g / kKS - 1)) break;
+        const Segment& s = segs[seg_k % kSegs];
+        load_tile(std::true_type{}, s, s.j0 + y_k * BN, st, bar(B_KFULL + st), slot_k, ids_k);
+        ++k_out;
+        ++y_k;
+        --left_k;
+      }
+      if (g >= 2) {
+        const int st = (g - 2) % kVS;
+        if (g - 2 >= kVS && !waits(B_VEMPTY + st, (g - 2) / kVS - 1)) break;
+        const Segment& s = segs[seg_v % kSegs];
+        // a partly masked tile goes to the rescale warps first, which then
+        // make the two arrivals on B_VFULL
+        const bool part = y_v < s.fa || y_v >= s.fb;
+        if (part) {
+          raw |= 1u << st;
+          raw_next ^= 1u << st;
+        } else {
+          raw &= ~(1u << st);
+          if (lane == 0) mbar_arrive(bar(B_VFULL + st));
+        }
+        load_tile(std::false_type{}, s, s.j0 + y_v * BN, st, bar((part ? B_VRAW : B_VFULL) + st),
+                  slot_v, ids_v);
+        ++v_out;
+        ++y_v;
+        --left_v;
+      }
+    }
+    // no copy may still be landing in this CTA's shared memory at exit
+    for (int t = max(0, k_out - kKS); t < k_out; ++t)
+      mbar_wait(bar(B_KFULL + t % kKS), (t / kKS) & 1, a.status);
+    for (int t = max(0, v_out - kVS); t < v_out; ++t) {
+      const int st = t % kVS;
+      if ((raw >> st) & 1u) mbar_wait(bar(B_VRAW + st), ((raw_next >> st) & 1u) ^ 1u, a.status);
+      else mbar_wait(bar(B_VFULL + st), (t / kVS) & 1, a.status);
+    }
+    if (q_out > 0) mbar_wait(bar(B_QFULL), (q_out - 1) & 1, a.status);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
     if (lane == 0) {
       const uint32_t idesc_qk = idesc_bf16(BM, BN, false, false);
       const uint32_t idesc_pv = idesc_bf16(BM, V, false, true);
-      // two walks over the CTA's tiles: S runs two tiles ahead of P V
-      Cursor cq = c;
-      long long xq = x0;
-      Segment sq = segment_of(cq, x1 - xq);
-      int seg_q = 0, tq = sq.ta;
+      // S runs two tiles ahead of P V, each with its own count of segments
+      int seg_q = -1, left_q = 0, seg_p = -1, left_p = 0;
+      auto tiles_of = [&](int seg) {
+        return wait_bar(bar(B_SEG + seg % kSegs), (seg / kSegs) & 1, a.status, abort_flag)
+                   ? *reinterpret_cast<volatile int*>(&segs[seg % kSegs].cnt) : 0;
+      };
       auto issue_qk = [&](int g) -> bool {
-        if (tq == sq.tb) {  // the next unit's rows
-          xq += sq.tb - sq.ta;
-          next_unit<BM>(a.bt, a.window, HQ, pk, cq);
-          sq = segment_of(cq, x1 - xq);
-          tq = sq.ta;
-          ++seg_q;
+        if (left_q == 0) {  // the next unit's rows
+          left_q = tiles_of(++seg_q);
+          if (left_q == 0 || !wait_bar(bar(B_QFULL), seg_q & 1, a.status, abort_flag)) return false;
         }
         const int st = g % kKS;
-        if (tq == sq.ta && !wait_bar(bar(B_QFULL), seg_q & 1, a.status, abort_flag)) return false;
         if (!wait_bar(bar(B_KREADY + st), (g / kKS) & 1, a.status, abort_flag)) return false;
         tc_fence_after();
         const uint32_t d_tmem = tmem + (g & 1) * 128;
@@ -343,28 +393,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         umma_commit(bar(B_SFULL + (g & 1)));
         umma_commit(bar(B_KEMPTY + st));
-        if (++tq == sq.tb) umma_commit(bar(B_QEMPTY));
+        if (--left_q == 0) umma_commit(bar(B_QEMPTY));
         return true;
       };
       bool ok = issue_qk(0);
       if (ok && n_tiles > 1) ok = issue_qk(1);
-      int seg = 0;
-      long long x = x0;
-      Segment s = segment_of(c, x1 - x);
-      int t = s.ta;
       uint32_t begun = 0;  // groups with a tile in this segment
       for (int g = 0; ok && g < n_tiles; ++g) {
-        if (t == s.tb) {
-          x += s.tb - s.ta;
-          next_unit<BM>(a.bt, a.window, HQ, pk, c);
-          s = segment_of(c, x1 - x);
-          t = s.ta;
-          ++seg;
-          begun = 0;
-        }
         const int grp = g & 1, vs = g % kVS;
-        if (t == s.ta && seg > 0 &&
-            !wait_bar(bar(B_OEMPTY), (seg - 1) & 1, a.status, abort_flag)) break;
+        if (left_p == 0) {
+          left_p = tiles_of(++seg_p);
+          begun = 0;
+          if (left_p == 0) break;
+          if (seg_p > 0 && !wait_bar(bar(B_OEMPTY), (seg_p - 1) & 1, a.status, abort_flag)) break;
+        }
         if (!wait_bar(bar(B_VFULL + vs), (g / kVS) & 1, a.status, abort_flag)) break;
         if (!wait_bar(bar(B_PFULL + grp), (g >> 1) & 1, a.status, abort_flag)) break;
         tc_fence_after();
@@ -381,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         begun |= 1u << grp;
         umma_commit(bar(B_PVDONE + grp));
         umma_commit(bar(B_VEMPTY + vs));
-        ++t;
+        --left_p;
         if (g + 2 < n_tiles) ok = issue_qk(g + 2);
       }
       // every MMA of this CTA has completed before TMEM is released
@@ -392,82 +434,96 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ key rescale
     constexpr int kChunks = KD / 8;          // 16-byte chunks per row
     constexpr int kRowStep = 64 / kChunks;   // rows covered by one pass of 64 threads
+    constexpr int kBatch = 32 / kRowStep;    // rows a thread has of 32
     const int tid = threadIdx.x - 64;
     const int ch = tid % kChunks;
     const int rs = tid / kChunks;
-    int g = 0;
     uint32_t raw = 0;  // parity of each value stage's next partly masked tile
+    int g = 0;
     bool ok = true;
-    for (long long x = x0; ok && x < x1;) {
-      const Segment s = segment_of(c, x1 - x);
-      const int slot_i = s.pos0 >> a.shift;
-      const int page_i = !c.r.dead && slot_i < a.MP
-                             ? page_of(a.table, (long)c.r.i * a.MP, slot_i, a.NP) : -1;
+    for (int seg = 0; ok && g < n_tiles; ++seg) {
+      if (!__all_sync(0xffffffffu, wait_bar(bar(B_SEG + seg % kSegs), (seg / kSegs) & 1, a.status,
+                                            abort_flag)))
+        break;
+      const Segment s = segs[seg % kSegs];
       int ri[8];
+      if (s.page_i >= 0) {
+        const int4* r4 = reinterpret_cast<const int4*>(a.rp + ((long)s.page_i * a.HQ + s.h) * KD + ch * 8);
+        const int4 u = __ldg(r4), w = __ldg(r4 + 1);
+        ri[0] = u.x; ri[1] = u.y; ri[2] = u.z; ri[3] = u.w;
+        ri[4] = w.x; ri[5] = w.y; ri[6] = w.z; ri[7] = w.w;
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        ri[e] = page_i >= 0 ? __ldg(a.rp + ((long)page_i * HQ + c.h) * KD + ch * 8 + e) : 0;
-      const int seen_from = max(0, s.pos0 - win + 1);
+        for (int e = 0; e < 8; ++e) ri[e] = 0;
+      }
       bool flag = false;
-      for (int t = s.ta; t < s.tb; ++t, ++g) {
+      for (int y = 0; y < s.cnt; ++y, ++g) {
         const int st = g % kKS;
-        {
-          const bool got = wait_bar(bar(B_KFULL + st), (g / kKS) & 1, a.status, abort_flag);
-          if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, wait_bar(bar(B_KFULL + st), (g / kKS) & 1, a.status, abort_flag))) {
+          ok = false;
+          break;
         }
-        const int j0 = (s.lo + t) * BN;
-        const int nk = c.r.dead ? 0 : min(BN, c.r.kv - j0);
-        const int np = (nk + PS - 1) >> a.shift;
+        const int j0 = s.j0 + y * BN;
         uint8_t* kt = smem + Lay::oK + st * Lay::kT + (ch / 8) * (BN * 128);
-        for (int y = 0; y < np; ++y) {
-          const int* rc = reinterpret_cast<const int*>(smem + Lay::oR) + (st * Lay::kRows + y) * KD + ch * 8;
+#pragma unroll 1
+        for (int z0 = 0; z0 < BN / 32; ++z0) {
+          // 2^(R_I - R_c) of the page that holds these 32 rows (rows past the
+          // request's last page hold what an earlier tile left: scaled along,
+          // and masked)
+          const int pg = z0 * 32 >> a.shift;
+          const int4* rc = reinterpret_cast<const int4*>(
+              reinterpret_cast<const int*>(smem + Lay::oR) + (st * Lay::kRows + pg) * KD + ch * 8);
+          uint4 w[kBatch];
+#pragma unroll
+          for (int z = 0; z < kBatch; ++z) {
+            const int r = z0 * 32 + rs + z * kRowStep;
+            w[z] = *reinterpret_cast<const uint4*>(kt + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+          }
+          const int4 u = rc[0], v = rc[1];
+          const int d[8] = {ri[0] - u.x, ri[1] - u.y, ri[2] - u.z, ri[3] - u.w,
+                            ri[4] - v.x, ri[5] - v.y, ri[6] - v.z, ri[7] - v.w};
+          int most = d[0];
+#pragma unroll
+          for (int e = 1; e < 8; ++e) most = max(most, d[e]);
+          // beyond the operands' range, on a key that some row sees
+          if (most > (int)kAnchorRange)
+            flag |= j0 + z0 * 32 < min(s.kv, s.pos0 + s.ni) && j0 + z0 * 32 + 32 > s.from;
           __nv_bfloat162 f[4];
-          bool far = false;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int e0 = ri[2 * e] - rc[2 * e], e1 = ri[2 * e + 1] - rc[2 * e + 1];
-            far |= max(e0, e1) > (int)kAnchorRange;
-            const uint32_t b = pow2_bf16(e0) | (pow2_bf16(e1) << 16);
+            const uint32_t b = pow2_bf16(d[2 * e]) | (pow2_bf16(d[2 * e + 1]) << 16);
             f[e] = *reinterpret_cast<const __nv_bfloat162*>(&b);
           }
-          // a page wholly before the window may be gone: nothing is seen of it
-          flag |= far && j0 + ((y + 1) << a.shift) > seen_from && j0 + (y << a.shift) < s.pos0 + s.ni;
-          constexpr int kBatch = 32 / kRowStep;  // a 32-row piece of a page
-#pragma unroll 1
-          for (int r0 = y << a.shift; r0 < ((y + 1) << a.shift); r0 += 32) {
-            uint4 w[kBatch];
 #pragma unroll
-            for (int z = 0; z < kBatch; ++z) {
-              const int r = r0 + rs + z * kRowStep;
-              w[z] = *reinterpret_cast<const uint4*>(kt + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
-            }
+          for (int z = 0; z < kBatch; ++z) {
+            const int r = z0 * 32 + rs + z * kRowStep;
+            __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&w[z]);
 #pragma unroll
-            for (int z = 0; z < kBatch; ++z) {
-              const int r = r0 + rs + z * kRowStep;
-              __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&w[z]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], f[e]);
-              *reinterpret_cast<uint4*>(kt + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = w[z];
-            }
+            for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], f[e]);
+            *reinterpret_cast<uint4*>(kt + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = w[z];
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_KREADY + st));
-        if (!sees_all(s, c.r.dead, j0, win)) {
+        if (y < s.fa || y >= s.fb) {
           const int vs = g % kVS;
-          const bool got = wait_bar(bar(B_VRAW + vs), (raw >> vs) & 1u, a.status, abort_flag);
-          if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+          if (!__all_sync(0xffffffffu, wait_bar(bar(B_VRAW + vs), (raw >> vs) & 1u, a.status, abort_flag))) {
+            ok = false;
+            break;
+          }
           raw ^= 1u << vs;
+          const int nk = s.kv - j0;
           uint8_t* vt = smem + Lay::oV + vs * Lay::kT + (ch / 8) * (BN * 128);
           uint32_t bad = 0;
+#pragma unroll 4
           for (int r = rs; r < BN; r += kRowStep) {
             uint4* w = reinterpret_cast<uint4*>(vt + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
             if (r >= nk) {
               *w = make_uint4(0u, 0u, 0u, 0u);
             } else {
-              const uint4 y = *w;
-              bad |= not_finite(y.x) | not_finite(y.y) | not_finite(y.z) | not_finite(y.w);
+              const uint4 x = *w;
+              bad |= not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w);
             }
           }
           flag |= bad != 0;
@@ -476,9 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(bar(B_VFULL + vs));
         }
       }
-      if (flag) flags.set(c.r, c.b, c.h, HQ);
-      x += s.tb - s.ta;
-      if (ok && x < x1) next_unit<BM>(a.bt, a.window, HQ, pk, c);
+      if (flag) flags.set(s.place, s.h, a.HQ);
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -489,27 +543,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_addr = tmem + lane_base + grp * 128;
     const uint32_t o_addr = tmem + lane_base + 256 + grp * V;
     const float sl2 = a.scale_log2;
-    int g0 = 0, n_seg = 0;  // the CTA's tiles before the segment
+    int g0 = 0;  // the CTA's tiles before the segment
     bool ok = true;
-    Cursor& cur = s_cur[warp - 4];
-    if (lane == 0) cur = c;
-    __syncwarp();
-    for (; ok && g0 < n_tiles; ++n_seg) {
-      const Segment s = segment_of(cur, n_tiles - g0);
-      const bool dead = cur.r.dead;
+    for (int seg = 0; ok && g0 < n_tiles; ++seg) {
+      if (!__all_sync(0xffffffffu, wait_bar(bar(B_SEG + seg % kSegs), (seg / kSegs) & 1, a.status,
+                                            abort_flag)))
+        break;
+      const Segment& s = segs[seg % kSegs];
+      const int cnt = s.cnt;
       const bool row_ok = r < s.ni;
-      const int i = s.pos0 + r;               // the row's position
       // a unit of few rows leaves whole warps without one: they keep step only
       const bool idle = quarter * 32 >= s.ni;
-      const int n_here = s.tb - s.ta;
       float m_use = -INFINITY, l = 0.f;
       const int first = (g0 + grp) & 1;       // this group's first tile of the segment
-      for (int y = first; y < n_here; y += 2) {
+      for (int y = first; y < cnt; y += 2) {
         const int g = g0 + y;
-        const int j0 = (s.lo + s.ta + y) * BN;
-        {
-          const bool got = wait_bar(bar(B_SFULL + grp), (g >> 1) & 1, a.status, abort_flag);
-          if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, wait_bar(bar(B_SFULL + grp), (g >> 1) & 1, a.status, abort_flag))) {
+          ok = false;
+          break;
         }
         if (idle) {
           __syncwarp();
@@ -517,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         tc_fence_after();
-        const bool fast = sees_all(s, dead, j0, win);  // the same for the whole CTA
+        const bool fast = y >= s.fa && y < s.fb;  // the same for the whole CTA
         bool done = false;
         // One pass when every row's running max is set: exponentials against
         // it, kept in registers and stored only if no row's sum exceeds
@@ -554,41 +605,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!done) {
-          // pass 1: row max
-          float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
           // the row's visible keys of the tile: [ja, jb)
-          const int jb = row_ok && !dead ? min(BN, i + 1 - j0) : 0;
-          const int ja = max(0, i - win + 1 - j0);
+          const int dist = s.pos0 + r - (s.j0 + y * BN);  // from the tile's first key to the row
+          const int jb = row_ok ? min(BN, dist + 1) : 0;
+          const int ja = a.window > 0 ? dist + 1 - a.window : 0;
+          // pass 1: row max
+          float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll 1
-          for (int cc = 0; cc < BN; cc += 64) {
-            uint32_t sv[64];
+          for (int cc = 0; cc < BN; cc += 32) {
+            uint32_t sv[32];
             tmem_ld32(s_addr + cc, sv);
-            tmem_ld32(s_addr + cc + 32, sv + 32);
             tmem_wait_ld();
             if (fast) {
 #pragma unroll
-              for (int e = 0; e < 64; e += 4) {
+              for (int e = 0; e < 32; e += 2) {
                 mx0 = fmaxf(mx0, __uint_as_float(sv[e]) * sl2);
                 mx1 = fmaxf(mx1, __uint_as_float(sv[e + 1]) * sl2);
-                mx2 = fmaxf(mx2, __uint_as_float(sv[e + 2]) * sl2);
-                mx3 = fmaxf(mx3, __uint_as_float(sv[e + 3]) * sl2);
               }
             } else {
 #pragma unroll
-              for (int e = 0; e < 64; ++e) {
+              for (int e = 0; e < 32; ++e) {
                 const bool vis = cc + e >= ja && cc + e < jb;
                 mx0 = fmaxf(mx0, vis ? __uint_as_float(sv[e]) * sl2 : -INFINITY);
               }
             }
           }
-          const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+          const float mx = fmaxf(mx0, mx1);
           const bool resc = mx > m_use + kRescaleThreshold;
           const float m_new = resc ? mx : m_use;
           const float alpha = m_use == -INFINITY ? 0.f : exp2f(m_use - m_new);
           if (y > first) {
             // this group's previous P V has landed in its O before O is rescaled
-            const bool got = wait_bar(bar(B_PVDONE + grp), ((g >> 1) - 1) & 1, a.status, abort_flag);
-            if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+            if (!__all_sync(0xffffffffu, wait_bar(bar(B_PVDONE + grp), ((g >> 1) - 1) & 1, a.status,
+                                                  abort_flag))) {
+              ok = false;
+              break;
+            }
             tc_fence_after();
             if (__any_sync(0xffffffffu, resc)) {
               const float f = resc ? alpha : 1.f;
@@ -614,23 +666,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t sv[32];
             tmem_ld32(s_addr + cc, sv);
             tmem_wait_ld();
-            float e32[32];
-            if (fast) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) e32[e] = exp2f(fmaf(__uint_as_float(sv[e]), sl2, -m_eff));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const bool vis = cc + e >= ja && cc + e < jb;
-                e32[e] = vis ? exp2f(fmaf(__uint_as_float(sv[e]), sl2, -m_eff)) : 0.f;
-              }
-            }
             uint32_t pk2[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              rs0 += e32[e];
-              rs1 += e32[e + 1];
-              pk2[e / 2] = pack_bf16x2(e32[e], e32[e + 1]);
+              float p0 = exp2f(fmaf(__uint_as_float(sv[e]), sl2, -m_eff));
+              float p1 = exp2f(fmaf(__uint_as_float(sv[e + 1]), sl2, -m_eff));
+              if (!fast) {
+                p0 = cc + e >= ja && cc + e < jb ? p0 : 0.f;
+                p1 = cc + e + 1 >= ja && cc + e + 1 < jb ? p1 : 0.f;
+              }
+              rs0 += p0;
+              rs1 += p1;
+              pk2[e / 2] = pack_bf16x2(p0, p1);
             }
             tmem_st16(s_addr + cc / 2, pk2);
           }
@@ -642,39 +689,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(B_PFULL + grp));
       }
       // ---- the unit's end, or the share's: merge the groups' (m, l, O)
-      const int mine = (n_here - first + 1) >> 1;          // this group's tiles
-      const int theirs = n_here - mine;
+      const int mine = (cnt - first + 1) >> 1;  // this group's tiles
       if (ok && mine > 0) {
         const int g_last = g0 + first + 2 * (mine - 1);
         ok = __all_sync(0xffffffffu, wait_bar(bar(B_PVDONE + grp), (g_last >> 1) & 1, a.status,
                                               abort_flag));
       }
-      float* xm = sX + (n_seg & 1) * (2 * 2 * BM);
+      float* xm = sX + (seg & 1) * (2 * 2 * BM);
       xm[(grp * 2) * BM + r] = m_use;
       xm[(grp * 2 + 1) * BM + r] = l;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_XCHG));
-      if (ok) ok = __all_sync(0xffffffffu, wait_bar(bar(B_XCHG), n_seg & 1, a.status, abort_flag));
+      if (ok) ok = __all_sync(0xffffffffu, wait_bar(bar(B_XCHG), seg & 1, a.status, abort_flag));
       if (ok) {
         tc_fence_after();
         const float m0 = xm[0 * BM + r], l0 = xm[1 * BM + r];
         const float m1 = xm[2 * BM + r], l1 = xm[3 * BM + r];
-        const bool has0 = grp == 0 ? mine > 0 : theirs > 0, has1 = grp == 0 ? theirs > 0 : mine > 0;
-        const bool whole = s.ta == 0 && s.tb == cur.n_tiles;
+        // the groups with a tile: both from two on
+        const bool has0 = cnt > 1 || (g0 & 1) == 0, has1 = cnt > 1 || (g0 & 1) == 1;
+        const bool whole = s.whole != 0;
+        const int h = s.h;
         float m_f = fmaxf(m0, m1);
-        if (whole && a.sink) m_f = fmaxf(m_f, a.sink[cur.h] * kLog2e);
+        if (whole && a.sink) m_f = fmaxf(m_f, a.sink[h] * kLog2e);
         const float a0 = m0 == -INFINITY ? 0.f : exp2f(m0 - m_f);
         const float a1 = m1 == -INFINITY ? 0.f : exp2f(m1 - m_f);
         float lt = l0 * a0 + l1 * a1;
         float inv = 1.f;
         if (whole) {
-          if (a.sink) lt += exp2f(a.sink[cur.h] * kLog2e - m_f);
+          if (a.sink) lt += exp2f(a.sink[h] * kLog2e - m_f);
           inv = lt > 0.f || lt != lt ? 1.f / lt : 0.f;  // a row that sees nothing: 0
         }
         const float f0 = a0 * inv, f1 = a1 * inv;
-        const int slot = s.ta == 0 ? 1 : 0;
-        __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.o) + ((long)(s.t0 + r) * HQ + cur.h) * V;
-        float* prow = parts.o(cta, slot, V) + (size_t)r * V;
+        const long row = (long)(s.t0 + r) * a.HQ + h;
         // each group writes half of the channels
         if (!idle) {
 #pragma unroll 1
@@ -683,28 +729,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (has0) tmem_ld32(tmem + lane_base + 256 + cc, ov0);
             if (has1) tmem_ld32(tmem + lane_base + 256 + V + cc, ov1);
             tmem_wait_ld();
-            float o32[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               // (a row whose weight is 0 had no key in the group: its O is 0)
-              float v = has0 ? __uint_as_float(ov0[e]) * f0 : 0.f;
-              if (has1) v = fmaf(__uint_as_float(ov1[e]), f1, v);
-              o32[e] = v;
+              float x = has0 ? __uint_as_float(ov0[e]) * f0 : 0.f;
+              if (has1) x = fmaf(__uint_as_float(ov1[e]), f1, x);
+              ov0[e] = __float_as_uint(x);
             }
             if (row_ok) {
               if (whole) {
-                uint4* dst = reinterpret_cast<uint4*>(orow + cc);
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + row * V + cc);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  dst[e] = make_uint4(pack_bf16x2(o32[8 * e], o32[8 * e + 1]),
-                                      pack_bf16x2(o32[8 * e + 2], o32[8 * e + 3]),
-                                      pack_bf16x2(o32[8 * e + 4], o32[8 * e + 5]),
-                                      pack_bf16x2(o32[8 * e + 6], o32[8 * e + 7]));
+                for (int e = 0; e < 4; ++e) {
+                  uint32_t pk[4];
+#pragma unroll
+                  for (int x = 0; x < 4; ++x)
+                    pk[x] = pack_bf16x2(__uint_as_float(ov0[8 * e + 2 * x]),
+                                        __uint_as_float(ov0[8 * e + 2 * x + 1]));
+                  dst[e] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                }
               } else {
-                float4* dst = reinterpret_cast<float4*>(prow + cc);
+                uint4* dst = reinterpret_cast<uint4*>(parts.o(cta, s.slot, V) + (size_t)r * V + cc);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                  dst[e] = make_float4(o32[4 * e], o32[4 * e + 1], o32[4 * e + 2], o32[4 * e + 3]);
+                  dst[e] = make_uint4(ov0[4 * e], ov0[4 * e + 1], ov0[4 * e + 2], ov0[4 * e + 3]);
               }
             }
           }
@@ -712,31 +760,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (grp == 0 && row_ok) {
           if (whole) {
-            if (a.lse)
-              a.lse[(long)(s.t0 + r) * HQ + cur.h] = lt == 0.f ? -INFINITY : (m_f + log2f(lt)) * kLn2;
+            if (a.lse) a.lse[row] = lt == 0.f ? -INFINITY : (m_f + log2f(lt)) * kLn2;
           } else {
-            float* pm = parts.ml(cta, slot, V) + r * 2;
+            float* pm = parts.ml(cta, s.slot, V) + r * 2;
             pm[0] = m_f;
             pm[1] = lt;
           }
         }
-        if (!whole && slot == 1 && warp == 4 && lane == 0) {
-          PartDesc d;
-          d.req = cur.r.i; d.h = cur.h; d.b = cur.b;
-          d.last_cta = sh.owner(sh.begin(cta) + g0 + cur.n_tiles - 1);
-          parts.desc[cta] = d;
-        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_OEMPTY));
-      g0 += n_here;
-      if (ok && g0 < n_tiles) {
-        Cursor nx = cur;
-        next_unit<BM>(a.bt, a.window, HQ, pk, nx);
-        __syncwarp();
-        if (lane == 0) cur = nx;
-        __syncwarp();
-      }
+      g0 += cnt;
     }
   }
   tc_fence_before();
@@ -792,7 +826,7 @@ __global__ void __launch_bounds__(256) chunk_queries_kernel(AttnArgs a, __nv_bfl
         wide |= fabsf(pv[e]) > kAnchorRange;
         qv[e] *= exp2f(pv[e]);
       }
-      if (wide) flags.set(r, b, off / a.K, a.HQ);
+      if (wide) flags.set(flags.place(r, b), off / a.K, a.HQ);
       store8(qh + (long)t * a.HQ * a.K + off, qv);
     }
   }
