@@ -116,7 +116,6 @@ __device__ __forceinline__ long long tiles_before(const Request& r, int b) {
   return s;
 }
 __device__ __forceinline__ long long tiles_per_head(const Request& r) {
-  if (r.nb == 0) return 0;
   return tiles_before(r, r.nb - 1) + unit_tiles(r, r.nb - 1);
 }
 
@@ -125,32 +124,55 @@ struct Pick {
   int n_min, n_max;
 };
 
-template <int TB>
-__device__ __forceinline__ long long request_tiles(const Batch& bt, int i, int window, int heads,
-                                                   const Pick& pk) {
+// What a CTA spends on a unit beside its tiles (its queries' load, the first
+// and the masked tiles' longer softmax, the epilogue) counts as U tiles in
+// front of them: a unit has U + tiles places.
+template <int TB, int U>
+__device__ __forceinline__ long long request_places(const Batch& bt, int i, int window, int heads,
+                                                    const Pick& pk) {
   const int n = bt.rows(i);
-  if (n < pk.n_min || n > pk.n_max) return 0;
-  return heads * tiles_per_head(request_of<TB>(bt, i, window));
+  if (n < pk.n_min || n > pk.n_max || n == 0) return 0;
+  const Request r = request_of<TB>(bt, i, window);
+  return heads * (tiles_per_head(r) + (long long)U * r.nb);
 }
 
-// A CTA's position in the flattened tiles (request, head, block, tile).
+// A CTA's position in the flattened places (request, head, block, place).
 struct Cursor {
   Request r;
   int h, b;      // unit
-  int t;         // next tile of the unit, counted from 0
+  int p;         // place in the unit
   int n_tiles;   // the unit's tiles
 };
+// The tiles [ta, tb) of the unit among the next `left` places, and how many of
+// the places the unit takes.  (ta == tb: only places before its first tile.)
+struct Run {
+  int ta, tb, places;
+};
+template <int U>
+__device__ __forceinline__ Run run_of(const Cursor& c, long long left) {
+  Run r;
+  const long long to_end = U + c.n_tiles - c.p;
+  r.places = (int)(left < to_end ? left : to_end);
+  r.ta = max(0, c.p - U);
+  r.tb = max(0, c.p + r.places - U);
+  return r;
+}
 
-// The division: CTA c of G takes tiles [W c / G, W (c+1) / G) of the W tiles
-// of the batch, so every CTA gets the same work to within one tile, whatever
-// the lengths.  A unit cut by a boundary is joined afterwards from its parts.
+// The division: CTA c of G takes places [W c / G, W (c+1) / G) of the batch's
+// W, so every CTA gets the same work to within one tile, whatever the lengths.
+// A unit cut by a boundary is joined afterwards from its parts.
 struct Share {
   long long W;
   int G;
   __device__ __forceinline__ long long begin(int c) const { return W * c / G; }
-  // the CTA that holds tile x
+  // the CTA that holds place x
   __device__ __forceinline__ int owner(long long x) const {
     return (int)(((x + 1) * G + W - 1) / W) - 1;
+  }
+  // the CTA that holds the last tile of a unit whose place p is place x
+  template <int U>
+  __device__ __forceinline__ int last_owner(const Cursor& c, long long x) const {
+    return owner(x - c.p + U + c.n_tiles - 1);
   }
 };
 
@@ -172,21 +194,18 @@ __device__ __forceinline__ long long warp_incl_sum(long long x) {
 }
 
 // Called by all threads of the CTA.  Fills `sh` (the division) and, when this
-// CTA has work, `fs.req` and `fs.base`: the request that holds its first tile
-// and the tiles before that request.  min_tiles: no more CTAs share the work
-// than leave each that many tiles.
-template <int TB>
+// CTA has work, `fs.req` and `fs.base`: the request that holds its first place
+// and the places before that request.  No more CTAs share the work than leave
+// each `least` places.
+template <int TB, int U>
 __device__ __forceinline__ bool find_start(const Batch& bt, int window, int heads, const Pick& pk,
-                                           int min_tiles, int cta, int n_cta, FindScratch& fs,
+                                           int least, int cta, int n_cta, FindScratch& fs,
                                            Share& sh) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int nw = (nt + 31) >> 5;
-  long long mine = 0, one = 0;
-  for (int i = tid; i < bt.N; i += nt) {
-    one = request_tiles<TB>(bt, i, window, heads, pk);
-    mine += one;
-  }
-  // total (and, when each thread holds one request, the scan itself)
+  long long mine = 0;
+  for (int i = tid; i < bt.N; i += nt) mine += request_places<TB, U>(bt, i, window, heads, pk);
+  // the total (and, when each thread has one request, the scan itself)
   const long long incl = warp_incl_sum(mine);
   if (lane == 31) fs.warp_sum[warp] = incl;
   __syncthreads();
@@ -198,7 +217,7 @@ __device__ __forceinline__ bool find_start(const Batch& bt, int window, int head
   }
   __syncthreads();
   sh.W = fs.total;
-  const long long most = (sh.W + min_tiles - 1) / min_tiles;
+  const long long most = (sh.W + least - 1) / least;
   sh.G = (int)(most < n_cta ? most : n_cta);
   if (cta >= sh.G) return false;
   const long long x = sh.begin(cta);
@@ -214,7 +233,7 @@ __device__ __forceinline__ bool find_start(const Batch& bt, int window, int head
   long long before = 0;
   for (int i0 = 0; i0 < bt.N; i0 += nt) {
     const int i = i0 + tid;
-    one = i < bt.N ? request_tiles<TB>(bt, i, window, heads, pk) : 0;
+    const long long one = i < bt.N ? request_places<TB, U>(bt, i, window, heads, pk) : 0;
     const long long in1 = warp_incl_sum(one);
     __syncthreads();
     if (lane == 31) fs.warp_sum[warp] = in1;
@@ -233,33 +252,33 @@ __device__ __forceinline__ bool find_start(const Batch& bt, int window, int head
   return true;
 }
 
-// The cursor at flattened tile x, x inside request `req`, which begins at `base`.
-template <int TB>
+// The cursor at flattened place x, x inside request `req`, which begins at `base`.
+template <int TB, int U>
 __device__ __forceinline__ Cursor cursor_at(const Batch& bt, int window, int req, long long base,
                                             long long x) {
   Cursor c;
   c.r = request_of<TB>(bt, req, window);
   long long rem = x - base;
-  const long long per_head = tiles_per_head(c.r);
+  const long long per_head = tiles_per_head(c.r) + (long long)U * c.r.nb;
   c.h = (int)(rem / per_head);
   rem -= c.h * per_head;
   int lo = 0, hi = c.r.nb - 1;  // the last block that begins at or before rem
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (tiles_before(c.r, mid) <= rem) lo = mid;
+    if (tiles_before(c.r, mid) + (long long)U * mid <= rem) lo = mid;
     else hi = mid - 1;
   }
   c.b = lo;
-  c.t = (int)(rem - tiles_before(c.r, lo));
+  c.p = (int)(rem - tiles_before(c.r, lo) - (long long)U * lo);
   c.n_tiles = unit_tiles(c.r, lo);
   return c;
 }
 
-// To the next unit.
+// To the next unit (there is one: the caller's places do not end here).
 template <int TB>
 __device__ __forceinline__ void next_unit(const Batch& bt, int window, int heads, const Pick& pk,
                                           Cursor& c) {
-  c.t = 0;
+  c.p = 0;
   if (++c.b == c.r.nb) {
     c.b = 0;
     if (++c.h == heads) {
@@ -269,7 +288,7 @@ __device__ __forceinline__ void next_unit(const Batch& bt, int window, int heads
         const int n = bt.rows(i);
         if (n >= pk.n_min && n <= pk.n_max && n > 0) break;
       }
-      if (i >= bt.N) return;  // the caller's tile count ends here
+      if (i >= bt.N) return;
       c.r = request_of<TB>(bt, i, window);
     }
   }

@@ -182,11 +182,12 @@ __global__ void __launch_bounds__(kGenThreads) general_kernel(AttnArgs a, Pick p
   const int cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) parts.desc[cta].last_cta = -1;
   Share sh;
-  if (!find_start<GR>(a.bt, a.window, a.HQ, pk, 1, cta, parts.n_cta, fs, sh)) return;
+  if (!find_start<GR, 0>(a.bt, a.window, a.HQ, pk, 1, cta, parts.n_cta, fs, sh)) return;
   const long long x0 = sh.begin(cta), x1 = sh.begin(cta + 1);
-  Cursor c = cursor_at<GR>(a.bt, a.window, fs.req, fs.base, x0);
+  Cursor c = cursor_at<GR, 0>(a.bt, a.window, fs.req, fs.base, x0);
   for (long long x = x0; x < x1;) {
-    const int ta = c.t, tb = (int)min((long long)c.n_tiles, ta + (x1 - x));
+    const Run run = run_of<0>(c, x1 - x);
+    const int ta = run.ta, tb = run.tb;
     float m[kRowsPerWarp], l[kRowsPerWarp], acc[kRowsPerWarp][4];
     gen_tiles<T>(a, c.r, c.h, c.b * GR, tile_lo(c.r, c.b), ta, tb, gen_shared, m, l, acc);
     const int ni = min(GR, c.r.n - c.b * GR);
@@ -213,10 +214,10 @@ __global__ void __launch_bounds__(kGenThreads) general_kernel(AttnArgs a, Pick p
     if (!whole && slot == 1 && threadIdx.x == 0) {
       PartDesc d;
       d.req = c.r.i; d.h = c.h; d.b = c.b;
-      d.last_cta = sh.owner(x + c.n_tiles - 1);
+      d.last_cta = sh.last_owner<0>(c, x);
       parts.desc[cta] = d;
     }
-    x += tb - ta;
+    x += run.places;
     if (x < x1) next_unit<GR>(a.bt, a.window, a.HQ, pk, c);
   }
 }

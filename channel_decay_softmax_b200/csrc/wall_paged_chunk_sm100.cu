@@ -53,13 +53,14 @@ constexpr int kKS = 3;                    // key stages
 constexpr int kVS = 2;                    // value stages
 constexpr float kRescaleThreshold = 8.f;  // log2 units: lazy O rescale
 constexpr float kRescaleBound = 256.f;    // 2^kRescaleThreshold
+constexpr int kUnit = 3;                  // a unit's own cost, in tiles
 
 // A CTA's piece of one unit, as every role reads it.
 struct Segment {
   int t0, ni;       // first query row among the packed ones, rows
   int pos0;         // position of the first row (far below 0 where the request sees nothing)
   int j0;           // first key of its first tile
-  int cnt;          // tiles
+  int cnt;          // tiles (0: the CTA's share has ended)
   int fa, fb;       // tiles [fa, fb) are seen whole by every row
   int kv;           // keys of the request (0 where it sees nothing)
   int from;         // first key that any row sees
@@ -69,7 +70,7 @@ struct Segment {
   int place;        // of its flag
   int whole;        // the unit lies in this CTA alone
   int slot;         // else its part's slot
-  int last_cta;     // and the CTA that ends it
+  int pad;
 };
 static_assert(sizeof(Segment) == 64, "four 16-byte words");
 // Segments in flight: warp 0 writes the entry of segment s + 8 when its first
@@ -141,6 +142,32 @@ __device__ __forceinline__ uint32_t pow2_bf16(int e) {
   return e < -126 ? 0u : e > 127 ? 0x7F80u : uint32_t(e + 127) << 7;
 }
 
+// Low word of a 128-byte-swizzle shared-memory descriptor (see sdesc_sw128);
+// the high word is the same for all of this kernel's: stride 1024 between
+// 8-row groups, version, swizzle mode.
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
+}
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t keep) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(keep), "r"(kDescHi));
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t keep) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(keep), "r"(kDescHi));
+}
+
 // Any half of the word that is an infinity or a NaN
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
   return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
@@ -195,8 +222,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
   }
   Share sh;
-  if (!find_start<BM>(a.bt, a.window, a.HQ, {2, 0x7fffffff}, 2, cta, parts.n_cta, fs, sh)) return;
-  const int n_tiles = (int)(sh.begin(cta + 1) - sh.begin(cta));  // of this CTA
+  if (!find_start<BM, kUnit>(a.bt, a.window, a.HQ, {2, 0x7fffffff}, kUnit + 2, cta, parts.n_cta, fs,
+                             sh))
+    return;
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_holder), 512);
     tmem_relinquish();
@@ -227,43 +255,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto table_at = [&](int req, int slot) {
       return slot + lane < a.MP ? page_of(a.table, (long)req * a.MP, slot + lane, a.NP) : -1;
     };
-    Cursor c = cursor_at<BM>(a.bt, a.window, fs.req, fs.base, sh.begin(cta));
+    long long x = sh.begin(cta);
+    const long long x1 = sh.begin(cta + 1);
+    Cursor c = cursor_at<BM, kUnit>(a.bt, a.window, fs.req, fs.base, x);
     int slot_k = 0, ids_k = 0, seg_k = -1;
-    // the figures of the cursor's unit, of which this CTA has `left` tiles at
-    // most, into the ring; returns its number of tiles
-    auto open_segment = [&](int left) {
-      const int lo = tile_lo(c.r, c.b);
+    // the figures of the next unit that this CTA has tiles of, into the ring;
+    // returns their number, 0 at the share's end
+    auto open_segment = [&]() {
       Segment s;
-      s.t0 = c.r.t0 + c.b * BM;
-      s.ni = min(BM, c.r.n - c.b * BM);
-      s.pos0 = c.r.dead ? -(1 << 29) : c.r.ctx + c.b * BM;
-      s.j0 = (lo + c.t) * BN;
-      s.cnt = min(c.n_tiles - c.t, left);
-      // seen whole: the first row sees its last key, the last row its first
-      s.fa = c.r.dead ? 0 : max(0, (max(s.pos0 + s.ni - win, 0) - s.j0 + BN - 1) >> 7);
-      s.fb = c.r.dead ? 0 : max(0, (s.pos0 + 1 - s.j0) >> 7);
-      s.kv = c.r.dead ? 0 : c.r.kv;
-      s.from = c.r.dead ? 0 : max(0, s.pos0 - win + 1);
-      s.h = c.h;
-      s.req = c.r.i;
-      slot_k = s.j0 >> a.shift;
-      ids_k = c.r.dead ? -1 : table_at(s.req, slot_k);
-      const int slot_i = s.pos0 >> a.shift;  // (one entry, the same for every lane)
-      s.page_i = !c.r.dead && slot_i < a.MP ? page_of(a.table, (long)s.req * a.MP, slot_i, a.NP) : -1;
-      s.place = (int)flags.place(c.r, c.b);
-      s.whole = c.t == 0 && s.cnt == c.n_tiles;
-      s.slot = c.t == 0 ? 1 : 0;
-      s.last_cta = -1;
-      if (c.t == 0 && !s.whole) s.last_cta = sh.owner(sh.begin(cta) + (n_tiles - left) + c.n_tiles - 1);
+      s.cnt = 0;
+      while (x < x1) {
+        const Run run = run_of<kUnit>(c, x1 - x);
+        if (run.tb > run.ta) {
+          s.t0 = c.r.t0 + c.b * BM;
+          s.ni = min(BM, c.r.n - c.b * BM);
+          s.pos0 = c.r.dead ? -(1 << 29) : c.r.ctx + c.b * BM;
+          s.j0 = (tile_lo(c.r, c.b) + run.ta) * BN;
+          s.cnt = run.tb - run.ta;
+          // seen whole: the first row sees its last key, the last row its first
+          s.fa = c.r.dead ? 0 : max(0, (max(s.pos0 + s.ni - win, 0) - s.j0 + BN - 1) >> 7);
+          s.fb = c.r.dead ? 0 : max(0, (s.pos0 + 1 - s.j0) >> 7);
+          s.kv = c.r.dead ? 0 : c.r.kv;
+          s.from = c.r.dead ? 0 : max(0, s.pos0 - win + 1);
+          s.h = c.h;
+          s.req = c.r.i;
+          slot_k = s.j0 >> a.shift;
+          ids_k = c.r.dead ? -1 : table_at(s.req, slot_k);
+          const int slot_i = s.pos0 >> a.shift;  // (one entry, the same for every lane)
+          s.page_i = !c.r.dead && slot_i < a.MP
+                         ? page_of(a.table, (long)s.req * a.MP, slot_i, a.NP) : -1;
+          s.place = (int)flags.place(c.r, c.b);
+          s.whole = run.ta == 0 && run.tb == c.n_tiles;
+          s.slot = run.ta == 0 ? 1 : 0;
+          if (lane == 0 && run.ta == 0 && !s.whole) {
+            PartDesc d;
+            d.req = s.req; d.h = s.h; d.b = c.b;
+            d.last_cta = sh.last_owner<kUnit>(c, x);
+            parts.desc[cta] = d;
+          }
+        }
+        x += run.places;
+        if (x < x1) next_unit<BM>(a.bt, a.window, a.HQ, {2, 0x7fffffff}, c);
+        if (s.cnt > 0) break;
+      }
       ++seg_k;
       if (lane == 0) {
-        segs[seg_k % kSegs] = s;
+        if (s.cnt > 0) segs[seg_k % kSegs] = s;
+        else segs[seg_k % kSegs].cnt = 0;
         mbar_arrive(bar(B_SEG + seg_k % kSegs));
-        if (s.last_cta >= 0) {
-          PartDesc d;
-          d.req = s.req; d.h = s.h; d.b = c.b; d.last_cta = s.last_cta;
-          parts.desc[cta] = d;
-        }
       }
       __syncwarp();
       return s.cnt;
@@ -306,10 +345,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     int k_out = 0, v_out = 0, q_out = 0;
     uint32_t raw = 0, raw_next = 0;     // per value stage: its last tile is a partly masked one;
                                         // parity of the next one's B_VRAW phase
-    for (int g = 0; g < n_tiles + 2; ++g) {
+    bool more = true;                   // key tiles
+    for (int g = 0;; ++g) {
       if (g >= 2 && left_v == 0) {      // value tile g - 2 opens a segment: its queries
         const Segment& s = segs[++seg_v % kSegs];
         left_v = s.cnt;
+        if (left_v == 0) break;
         y_v = 0;
         slot_v = s.j0 >> a.shift;
         ids_v = s.kv > 0 ? table_at(s.req, slot_v) : -1;
@@ -320,19 +361,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(sbase + Lay::oQ + lane * (BM * 128), &tm_q, bar(B_QFULL), lane * 64, s.h, s.t0);
         ++q_out;
       }
-      if (g < n_tiles) {
+      if (more) {
         if (left_k == 0) {
-          if (g > 0) next_unit<BM>(a.bt, a.window, a.HQ, {2, 0x7fffffff}, c);
-          left_k = open_segment(n_tiles - g);
+          left_k = open_segment();
           y_k = 0;
+          more = left_k > 0;
         }
-        const int st = g % kKS;
-        if (g >= kKS && !waits(B_KEMPTY + st, g / kKS - 1)) break;
-        const Segment& s = segs[seg_k % kSegs];
-        load_tile(std::true_type{}, s, s.j0 + y_k * BN, st, bar(B_KFULL + st), slot_k, ids_k);
-        ++k_out;
-        ++y_k;
-        --left_k;
+        if (more) {
+          const int st = g % kKS;
+          if (g >= kKS && !waits(B_KEMPTY + st, g / kKS - 1)) break;
+          const Segment& s = segs[seg_k % kSegs];
+          load_tile(std::true_type{}, s, s.j0 + y_k * BN, st, bar(B_KFULL + st), slot_k, ids_k);
+          ++k_out;
+          ++y_k;
+          --left_k;
+        }
       }
       if (g >= 2) {
         const int st = (g - 2) % kVS;
@@ -367,64 +410,82 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
     if (lane == 0) {
-      const uint32_t idesc_qk = idesc_bf16(BM, BN, false, false);
-      const uint32_t idesc_pv = idesc_bf16(BM, V, false, true);
-      // S runs two tiles ahead of P V, each with its own count of segments
+      constexpr uint32_t idesc_qk = idesc_bf16(BM, BN, false, false);
+      constexpr uint32_t idesc_pv = idesc_bf16(BM, V, false, true);
+      // the descriptors' low words; what varies is the address
+      const uint32_t q_lo = sdesc_lo(sbase + Lay::oQ, 16);
+      const uint32_t k_lo = sdesc_lo(sbase + Lay::oK, 16);
+      const uint32_t v_lo = sdesc_lo(sbase + Lay::oV, BN * 128);
+      // S runs two tiles ahead of P V, each with its own count of segments and
+      // tiles; left_*: tiles of the segment still to be issued
       int seg_q = -1, left_q = 0, seg_p = -1, left_p = 0;
-      auto tiles_of = [&](int seg) {
-        return wait_bar(bar(B_SEG + seg % kSegs), (seg / kSegs) & 1, a.status, abort_flag)
-                   ? *reinterpret_cast<volatile int*>(&segs[seg % kSegs].cnt) : 0;
+      int gq = 0, st_q = 0;
+      uint32_t par_k = 0;
+      bool ok = true, more = true;  // key tiles
+      auto open = [&](int& seg, int& left) {
+        ++seg;
+        ok = wait_bar(bar(B_SEG + seg % kSegs), (seg / kSegs) & 1, a.status, abort_flag);
+        left = ok ? *reinterpret_cast<volatile int*>(&segs[seg % kSegs].cnt) : 0;
+        return left > 0;
       };
-      auto issue_qk = [&](int g) -> bool {
+      // S of the next key tile
+      auto issue_qk = [&]() {
         if (left_q == 0) {  // the next unit's rows
-          left_q = tiles_of(++seg_q);
-          if (left_q == 0 || !wait_bar(bar(B_QFULL), seg_q & 1, a.status, abort_flag)) return false;
+          more = open(seg_q, left_q);
+          if (!more) return;
+          ok = wait_bar(bar(B_QFULL), seg_q & 1, a.status, abort_flag);
+          if (!ok) return;
         }
-        const int st = g % kKS;
-        if (!wait_bar(bar(B_KREADY + st), (g / kKS) & 1, a.status, abort_flag)) return false;
+        ok = wait_bar(bar(B_KREADY + st_q), par_k, a.status, abort_flag);
+        if (!ok) return;
         tc_fence_after();
-        const uint32_t d_tmem = tmem + (g & 1) * 128;
+        const uint32_t d_tmem = tmem + (gq & 1) * 128;
+        const uint32_t kb = k_lo + st_q * (Lay::kT >> 4);
 #pragma unroll
         for (int kk = 0; kk < KD / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-          const uint64_t da = sdesc_sw128(sbase + Lay::oQ + off, 16, 1024);
-          const uint64_t db = sdesc_sw128(sbase + Lay::oK + st * Lay::kT + off, 16, 1024);
-          umma_bf16_ss(d_tmem, da, db, idesc_qk, kk > 0 ? 1u : 0u);
+          const uint32_t off = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
+          mma_ss(d_tmem, q_lo + off, kb + off, idesc_qk, kk > 0 ? 1u : 0u);
         }
-        umma_commit(bar(B_SFULL + (g & 1)));
-        umma_commit(bar(B_KEMPTY + st));
+        umma_commit(bar(B_SFULL + (gq & 1)));
+        umma_commit(bar(B_KEMPTY + st_q));
         if (--left_q == 0) umma_commit(bar(B_QEMPTY));
-        return true;
+        ++gq;
+        if (++st_q == kKS) {
+          st_q = 0;
+          par_k ^= 1;
+        }
       };
-      bool ok = issue_qk(0);
-      if (ok && n_tiles > 1) ok = issue_qk(1);
+      issue_qk();
+      if (ok && more) issue_qk();
       uint32_t begun = 0;  // groups with a tile in this segment
-      for (int g = 0; ok && g < n_tiles; ++g) {
-        const int grp = g & 1, vs = g % kVS;
+      for (int g = 0; ok && g < gq; ++g) {
+        const int grp = g & 1, vs = g & (kVS - 1);
         if (left_p == 0) {
-          left_p = tiles_of(++seg_p);
+          if (!open(seg_p, left_p)) break;
           begun = 0;
-          if (left_p == 0) break;
           if (seg_p > 0 && !wait_bar(bar(B_OEMPTY), (seg_p - 1) & 1, a.status, abort_flag)) break;
         }
         if (!wait_bar(bar(B_VFULL + vs), (g / kVS) & 1, a.status, abort_flag)) break;
         if (!wait_bar(bar(B_PFULL + grp), (g >> 1) & 1, a.status, abort_flag)) break;
         tc_fence_after();
         const uint32_t keep = (begun >> grp) & 1u;
+        const uint32_t vb = v_lo + vs * (Lay::kT >> 4);
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk) {
-          // A = P [128 rows x 16 keys] from TMEM (bf16 pairs over the S columns)
-          const uint32_t da = tmem + grp * 128 + kk * 8;
+        for (int kk = 0; kk < BN / 16; ++kk)
+          // A = P [128 rows x 16 keys] from TMEM (bf16 pairs over the S columns),
           // B = V [16 keys x V channels], MN-major
-          const uint64_t db =
-              sdesc_sw128(sbase + Lay::oV + vs * Lay::kT + kk * 16 * 128, BN * 128, 1024);
-          umma_bf16_ts(tmem + 256 + grp * V, da, db, idesc_pv, keep | (kk > 0 ? 1u : 0u));
-        }
+          mma_ts(tmem + 256 + grp * V, tmem + grp * 128 + kk * 8, vb + (kk * 16 * 128 >> 4), idesc_pv,
+                 kk > 0 ? 1u : keep);
         begun |= 1u << grp;
         umma_commit(bar(B_PVDONE + grp));
         umma_commit(bar(B_VEMPTY + vs));
         --left_p;
-        if (g + 2 < n_tiles) ok = issue_qk(g + 2);
+        // Two S in flight.  Where the next one opens a unit, its Qh may still
+        // be on its way: the last P V of this unit goes first.
+        if (more && !(left_q == 0 && left_p == 1)) {
+          issue_qk();
+          if (ok && more && gq == g + 2 && !(left_q == 0 && left_p == 1)) issue_qk();
+        }
       }
       // every MMA of this CTA has completed before TMEM is released
       umma_commit(bar(B_MMADONE));
@@ -441,11 +502,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t raw = 0;  // parity of each value stage's next partly masked tile
     int g = 0;
     bool ok = true;
-    for (int seg = 0; ok && g < n_tiles; ++seg) {
+    for (int seg = 0; ok; ++seg) {
       if (!__all_sync(0xffffffffu, wait_bar(bar(B_SEG + seg % kSegs), (seg / kSegs) & 1, a.status,
                                             abort_flag)))
         break;
       const Segment s = segs[seg % kSegs];
+      if (s.cnt == 0) break;
       int ri[8];
       if (s.page_i >= 0) {
         const int4* r4 = reinterpret_cast<const int4*>(a.rp + ((long)s.page_i * a.HQ + s.h) * KD + ch * 8);
@@ -545,12 +607,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sl2 = a.scale_log2;
     int g0 = 0;  // the CTA's tiles before the segment
     bool ok = true;
-    for (int seg = 0; ok && g0 < n_tiles; ++seg) {
+    for (int seg = 0; ok; ++seg) {
       if (!__all_sync(0xffffffffu, wait_bar(bar(B_SEG + seg % kSegs), (seg / kSegs) & 1, a.status,
                                             abort_flag)))
         break;
       const Segment& s = segs[seg % kSegs];
       const int cnt = s.cnt;
+      if (cnt == 0) break;
       const bool row_ok = r < s.ni;
       // a unit of few rows leaves whole warps without one: they keep step only
       const bool idle = quarter * 32 >= s.ni;

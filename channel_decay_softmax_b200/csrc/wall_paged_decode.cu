@@ -24,6 +24,7 @@ using namespace sm100;
 using namespace paged;
 
 constexpr int kTile = 32;
+constexpr int kUnit = 1;           // a unit's own cost, in tiles
 constexpr int kBox = kTile * 128;  // 64 channels of 32 rows
 
 struct DecodeLaunch {
@@ -68,56 +69,71 @@ __global__ void __launch_bounds__(288, 1)
     fence_barrier_init();
   }
   Share sh;
-  // two tiles a CTA at least: the join of more parts would cost what they save
-  if (!find_start<kTile>(a.bt, a.window, a.H, pk, 2, cta, parts.n_cta, fs, sh)) return;
+  // three places a CTA at least: the join of more parts would cost what they save
+  if (!find_start<kTile, kUnit>(a.bt, a.window, a.H, pk, 3, cta, parts.n_cta, fs, sh)) return;
   const long long x0 = sh.begin(cta), x1 = sh.begin(cta + 1);
-  Cursor c = cursor_at<kTile>(a.bt, a.window, fs.req, fs.base, x0);
+  Cursor c = cursor_at<kTile, kUnit>(a.bt, a.window, fs.req, fs.base, x0);
   if (warp == nw) {
     // ------------------------------------------------------------ TMA
+    // the lanes hold the next 32 entries of the block table; lane 0 copies
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
-      const uint32_t bytes = (uint32_t)(oR + G * KD * 4);
-      const uint64_t once = l2_evict_first();
-      int seq = 0;
-      bool ok = true;
-      int st = 0;
-      uint32_t phase = 1;  // of the empty barrier, from the second round on
-      for (long long x = x0; ok && x < x1; ++x) {
-        const int j0 = (tile_lo(c.r, c.b) + c.t) * kTile;
+    }
+    const uint32_t bytes = (uint32_t)(oR + G * KD * 4);
+    const uint64_t once = l2_evict_first();
+    const int PS1 = (1 << a.shift) - 1;
+    int seq = 0;
+    bool ok = true;
+    int st = 0;
+    uint32_t phase = 1;  // of the empty barrier, from the second round on
+    for (long long x = x0; ok && x < x1;) {
+      const Run run = run_of<kUnit>(c, x1 - x);
+      const int lo = tile_lo(c.r, c.b);
+      int slot0 = -32, ids = -1;
+      for (int t = run.ta; t < run.tb; ++t) {
+        const int j0 = (lo + t) * kTile;
         const int slot = j0 >> a.shift;
-        int page = slot < a.MP && !c.r.dead ? page_of(a.table, (long)c.r.i * a.MP, slot, a.NP) : -1;
-        if (page < 0 && !c.r.dead) record_status(a.status, WALL_ERR_INVALID_ARG);
-        if (seq >= stages && !mbar_wait(empty(st), phase, a.status)) {
+        if (slot >= slot0 + 32) {
+          slot0 = slot;
+          ids = !c.r.dead && slot + lane < a.MP
+                    ? page_of(a.table, (long)c.r.i * a.MP, slot + lane, a.NP) : -1;
+        }
+        const int page = __shfl_sync(0xffffffffu, ids, slot - slot0);
+        if (seq >= stages &&
+            !__all_sync(0xffffffffu, mbar_wait(empty(st), phase, a.status))) {
           ok = false;
           break;
         }
-        const uint32_t sb = sbase + st * dl.stage_bytes;
-        mbar_expect_tx(full(st), bytes);
-        const int off = j0 & ((1 << a.shift) - 1);
-        // a page that is none: past the pool's end, where the copy reads zeros
-        const int kz = page >= 0 ? page * a.HQ + c.h * G : a.NP * a.HQ;
-        const int vz = page >= 0 ? page * a.H + c.h : a.NP * a.H;
+        if (lane == 0) {
+          if (page < 0 && !c.r.dead) record_status(a.status, WALL_ERR_INVALID_ARG);
+          const uint32_t sb = sbase + st * dl.stage_bytes;
+          mbar_expect_tx(full(st), bytes);
+          // a page that is none: past the pool's end, where the copy reads zeros
+          const int kz = page >= 0 ? page * a.HQ + c.h * G : a.NP * a.HQ;
+          const int vz = page >= 0 ? page * a.H + c.h : a.NP * a.H;
 #pragma unroll
-        for (int bx = 0; bx < KD / 64; ++bx)
-          tma_load_3d_hint(sb + bx * G * kBox, &tm_k, full(st), bx * 64, off, kz, once);
+          for (int bx = 0; bx < KD / 64; ++bx)
+            tma_load_3d_hint(sb + bx * G * kBox, &tm_k, full(st), bx * 64, j0 & PS1, kz, once);
 #pragma unroll
-        for (int bx = 0; bx < VD / 64; ++bx)
-          tma_load_3d_hint(sb + oV + bx * kBox, &tm_v, full(st), bx * 64, off, vz, once);
-        bulk_load(sb + oR, a.rp + ((long)max(page, 0) * a.HQ + (long)c.h * G) * KD, G * KD * 4,
-                  full(st));
+          for (int bx = 0; bx < VD / 64; ++bx)
+            tma_load_3d_hint(sb + oV + bx * kBox, &tm_v, full(st), bx * 64, j0 & PS1, vz, once);
+          bulk_load(sb + oR, a.rp + ((long)max(page, 0) * a.HQ + (long)c.h * G) * KD, G * KD * 4,
+                    full(st));
+        }
+        __syncwarp();
         ++seq;
         if (++st == stages) {
           st = 0;
           phase ^= 1;
         }
-        if (++c.t == c.n_tiles && x + 1 < x1)
-          next_unit<kTile>(a.bt, a.window, a.H, pk, c);
       }
-      // no copy may still be landing when the CTA exits
-      for (int q = seq > stages ? seq - stages : 0; q < seq; ++q)
-        mbar_wait(full(q % stages), (uint32_t)((q / stages) & 1), a.status);
+      x += run.places;
+      if (x < x1) next_unit<kTile>(a.bt, a.window, a.H, pk, c);
     }
+    // no copy may still be landing when the CTA exits
+    for (int q = seq > stages ? seq - stages : 0; q < seq; ++q)
+      mbar_wait(full(q % stages), (uint32_t)((q / stages) & 1), a.status);
   } else if (warp < nw) {
     // ------------------------------------------------------------ query heads
     const int g = warp % G, par = warp / G;
@@ -129,7 +145,13 @@ __global__ void __launch_bounds__(288, 1)
     int n_seg = 0;
     bool ok = true;
     for (long long x = x0; x < x1;) {
-      const int ta = c.t, tb = (int)min((long long)c.n_tiles, ta + (x1 - x));
+      const Run run = run_of<kUnit>(c, x1 - x);
+      const int ta = run.ta, tb = run.tb;
+      if (ta == tb) {  // the unit's tiles are the next CTA's
+        x += run.places;
+        if (x < x1) next_unit<kTile>(a.bt, a.window, a.H, pk, c);
+        continue;
+      }
       const int kh = c.h, h = kh * G + g;
       const int pos = c.r.kv - 1;  // of the row; its request's last key
       const int lo_key = c.r.dead ? 0 : max(0, pos - win + 1);
@@ -320,14 +342,14 @@ __global__ void __launch_bounds__(288, 1)
             if (slot == 1 && g == 0) {
               PartDesc d;
               d.req = c.r.i; d.h = kh; d.b = 0;
-              d.last_cta = sh.owner(x + c.n_tiles - 1);
+              d.last_cta = sh.last_owner<kUnit>(c, x);
               parts.desc[cta] = d;
             }
           }
         }
       }
       ++n_seg;
-      x += tb - ta;
+      x += run.places;
       if (x < x1) next_unit<kTile>(a.bt, a.window, a.H, pk, c);
     }
   }

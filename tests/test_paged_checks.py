@@ -224,12 +224,32 @@ def test_unit_tiles_are_the_visible_ones(TB):
             total += r.tiles(b)
 
 
-def test_every_tile_has_one_owner():
+@pytest.mark.parametrize("U", [0, 1, 3])
+def test_every_tile_has_one_owner(U):
+    """Units of U + tiles places each, cut into even shares: every tile falls to
+    the one CTA that holds its place, a unit's tiles to neighbours, and the CTA
+    that ends a unit is the one its beginner names."""
     rng = random.Random(6)
-    for _ in range(200):
-        W, G = rng.randint(1, 5000), rng.randint(1, 600)
-        G = min(G, W)
-        owner = [((x + 1) * G + W - 1) // W - 1 for x in range(W)]
+    for _ in range(150):
+        units = [rng.randint(1, 40) for _ in range(rng.randint(1, 60))]
+        W = sum(U + n for n in units)
+        G = min(W, rng.randint(1, 300))
+        begin = [W * c // G for c in range(G + 1)]
+        owner = lambda x: ((x + 1) * G + W - 1) // W - 1
         for c in range(G):
-            assert all(owner[x] == c for x in range(W * c // G, W * (c + 1) // G))
-        assert owner[-1] == G - 1
+            assert all(owner(x) == c for x in range(begin[c], begin[c + 1]))
+        got = [[] for _ in units]  # (CTA, ta, tb) of each unit
+        for c in range(G):
+            x, base = begin[c], 0
+            for u, n in enumerate(units):
+                if base + U + n > begin[c] and base < begin[c + 1]:
+                    p = max(begin[c], base) - base
+                    places = min(begin[c + 1] - base - p, U + n - p)
+                    ta, tb = max(0, p - U), max(0, p + places - U)
+                    if tb > ta:
+                        got[u].append((c, ta, tb, owner(base + U + n - 1)))
+                base += U + n
+        for n, runs in zip(units, got):
+            assert runs[0][1] == 0 and runs[-1][2] == n
+            assert all(a[2] == b[1] and a[0] + 1 == b[0] for a, b in zip(runs, runs[1:]))
+            assert runs[0][3] == runs[-1][0]
