@@ -67,9 +67,9 @@ struct UnitFlags {
   __device__ __forceinline__ long place(const Request& r, int b) const {
     return (long)r.t0 / kChunkRows + r.i + b;
   }
-  __device__ __forceinline__ int* at(long place, int h, int HQ) const { return f + place * HQ + h; }
-  __device__ __forceinline__ void set(long place, int h, int HQ) const {
-    set_flag(at(place, h, HQ));
+  // unit: place * HQ + head
+  __device__ __forceinline__ void set(int unit, int HQ) const {
+    set_flag(f + unit);
     set_flag(any(HQ));
   }
 };

@@ -51,8 +51,8 @@ constexpr int BN = kChunkRows;
 constexpr int kThreads = 384;
 constexpr int kKS = 3;                    // key stages
 constexpr int kVS = 2;                    // value stages
-constexpr float kRescaleThreshold = 8.f;  // log2 units: lazy O rescale
-constexpr float kRescaleBound = 256.f;    // 2^kRescaleThreshold
+constexpr float kRaiseAbove = 256.f;      // a tile's sum of P that raises the row's reference
+constexpr float kFlagAbove = 1.2676506e30f;  // 2^100: one that may not be held
 constexpr int kUnit = 3;                  // a unit's own cost, in tiles
 
 // A CTA's piece of one unit, as every role reads it.
@@ -116,10 +116,11 @@ enum Bar {
 };
 static_assert(kNumBars <= Smem<128>::kBars, "barrier slots");
 
-// bounded wait that also gives up once another role has given up
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, int* status,
-                                         volatile int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
+// Bounded wait that also gives up once another role has given up.  The wait
+// itself is a call: inlined at each of its two dozen places it was a fifth of
+// the kernel's code.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, int* status,
+                                     volatile int* abort_flag) {
   const uint64_t t0 = global_timer_ns();
   for (;;) {
     if (mbar_try_wait_sleep(bar, parity, 100000u)) return true;
@@ -131,15 +132,29 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, int* sta
     }
   }
 }
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&h);
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, int* status,
+                                         volatile int* abort_flag) {
+  return mbar_try_wait(bar, parity) || wait_on(bar, parity, status, abort_flag);
+}
+// the same for a copy that has to land before the CTA may end
+__device__ __noinline__ void drain(uint32_t bar, uint32_t parity, int* status) {
+  mbar_wait(bar, parity, status);
 }
 
-// 2^e as bf16 bits: exact in the normal range, 0 below it
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// 2^e as bf16 bits: exact in the normal range, 0 below it, +inf above
 __device__ __forceinline__ uint32_t pow2_bf16(int e) {
-  return e < -126 ? 0u : e > 127 ? 0x7F80u : uint32_t(e + 127) << 7;
+  return uint32_t(min(max(e + 127, 0), 255)) << 7;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
 // Low word of a 128-byte-swizzle shared-memory descriptor (see sdesc_sw128);
@@ -171,6 +186,30 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_l
 // Any half of the word that is an infinity or a NaN
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
   return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+
+// A value tile of which nk rows are keys, by the 64 threads of the rescale
+// warps: the other rows become zeros; returns whether this thread saw a value
+// that is not finite among the keys'.
+template <int KD>
+__device__ __noinline__ bool clear_and_check(uint8_t* tile, int nk) {
+  constexpr int kChunks = KD / 8, kRowStep = 64 / kChunks;
+  const int tid = threadIdx.x - 64, ch = tid % kChunks;
+  uint8_t* vt = tile + (ch / 8) * (BN * 128);
+  uint32_t bad = 0;
+#pragma unroll 4
+  for (int r = tid / kChunks; r < BN; r += kRowStep) {
+    uint4* w = reinterpret_cast<uint4*>(vt + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+    if (r >= nk) {
+      *w = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      const uint4 x = *w;
+      bad |= not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  return bad != 0;
 }
 
 template <int KD>
@@ -400,13 +439,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // no copy may still be landing in this CTA's shared memory at exit
     for (int t = max(0, k_out - kKS); t < k_out; ++t)
-      mbar_wait(bar(B_KFULL + t % kKS), (t / kKS) & 1, a.status);
+      drain(bar(B_KFULL + t % kKS), (t / kKS) & 1, a.status);
     for (int t = max(0, v_out - kVS); t < v_out; ++t) {
       const int st = t % kVS;
-      if ((raw >> st) & 1u) mbar_wait(bar(B_VRAW + st), ((raw_next >> st) & 1u) ^ 1u, a.status);
-      else mbar_wait(bar(B_VFULL + st), (t / kVS) & 1, a.status);
+      if ((raw >> st) & 1u) drain(bar(B_VRAW + st), ((raw_next >> st) & 1u) ^ 1u, a.status);
+      else drain(bar(B_VFULL + st), (t / kVS) & 1, a.status);
     }
-    if (q_out > 0) mbar_wait(bar(B_QFULL), (q_out - 1) & 1, a.status);
+    if (q_out > 0) drain(bar(B_QFULL), (q_out - 1) & 1, a.status);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
     if (lane == 0) {
@@ -441,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t d_tmem = tmem + (gq & 1) * 128;
         const uint32_t kb = k_lo + st_q * (Lay::kT >> 4);
-#pragma unroll
+#pragma unroll 2
         for (int kk = 0; kk < KD / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
           mma_ss(d_tmem, q_lo + off, kb + off, idesc_qk, kk > 0 ? 1u : 0u);
@@ -455,10 +494,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           par_k ^= 1;
         }
       };
-      issue_qk();
-      if (ok && more) issue_qk();
       uint32_t begun = 0;  // groups with a tile in this segment
-      for (int g = 0; ok && g < gq; ++g) {
+      for (int g = 0; ok; ++g) {
+        // Two S in flight (S(g + 2) takes the place of P(g)).  Where the next
+        // one opens a unit, its Qh may still be on its way: the last P V of
+        // this unit goes first.
+#pragma unroll 1
+        while (ok && more && gq < g + 2 && !(left_q == 0 && gq == g + 1)) issue_qk();
+        if (!ok || g >= gq) break;
         const int grp = g & 1, vs = g & (kVS - 1);
         if (left_p == 0) {
           if (!open(seg_p, left_p)) break;
@@ -470,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t keep = (begun >> grp) & 1u;
         const uint32_t vb = v_lo + vs * (Lay::kT >> 4);
-#pragma unroll
+#pragma unroll 2
         for (int kk = 0; kk < BN / 16; ++kk)
           // A = P [128 rows x 16 keys] from TMEM (bf16 pairs over the S columns),
           // B = V [16 keys x V channels], MN-major
@@ -480,12 +523,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit(bar(B_PVDONE + grp));
         umma_commit(bar(B_VEMPTY + vs));
         --left_p;
-        // Two S in flight.  Where the next one opens a unit, its Qh may still
-        // be on its way: the last P V of this unit goes first.
-        if (more && !(left_q == 0 && left_p == 1)) {
-          issue_qk();
-          if (ok && more && gq == g + 2 && !(left_q == 0 && left_p == 1)) issue_qk();
-        }
       }
       // every MMA of this CTA has completed before TMEM is released
       umma_commit(bar(B_MMADONE));
@@ -499,9 +536,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x - 64;
     const int ch = tid % kChunks;
     const int rs = tid / kChunks;
+    const int PS = 1 << a.shift;
     uint32_t raw = 0;  // parity of each value stage's next partly masked tile
     int g = 0;
     bool ok = true;
+    auto check_values = [&](int gv, int nk, int unit) {
+      const int vs = gv % kVS;
+      if (!__all_sync(0xffffffffu, wait_bar(bar(B_VRAW + vs), (raw >> vs) & 1u, a.status, abort_flag)))
+        return false;
+      raw ^= 1u << vs;
+      if (clear_and_check<KD>(smem + Lay::oV + vs * Lay::kT, nk)) flags.set(unit, a.HQ);
+      if (lane == 0) mbar_arrive(bar(B_VFULL + vs));
+      return true;
+    };
+    int nk1 = -1, nk2 = -1, unit1 = 0, unit2 = 0;  // the last two tiles' (-1: seen whole)
     for (int seg = 0; ok; ++seg) {
       if (!__all_sync(0xffffffffu, wait_bar(bar(B_SEG + seg % kSegs), (seg / kSegs) & 1, a.status,
                                             abort_flag)))
@@ -527,74 +575,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int j0 = s.j0 + y * BN;
         uint8_t* kt = smem + Lay::oK + st * Lay::kT + (ch / 8) * (BN * 128);
-#pragma unroll 1
-        for (int z0 = 0; z0 < BN / 32; ++z0) {
-          // 2^(R_I - R_c) of the page that holds these 32 rows (rows past the
-          // request's last page hold what an earlier tile left: scaled along,
-          // and masked)
-          const int pg = z0 * 32 >> a.shift;
+        // 2^(R_I - R_c) of the page that begins at the tile's row 32 z (rows past
+        // the request's last page hold what an earlier tile left: scaled along,
+        // and masked)
+        uint32_t f0 = 0, f1 = 0, f2 = 0, f3 = 0;
+        auto factors = [&](int z) {
+          if ((z * 32 & (PS - 1)) != 0) return;
           const int4* rc = reinterpret_cast<const int4*>(
-              reinterpret_cast<const int*>(smem + Lay::oR) + (st * Lay::kRows + pg) * KD + ch * 8);
-          uint4 w[kBatch];
-#pragma unroll
-          for (int z = 0; z < kBatch; ++z) {
-            const int r = z0 * 32 + rs + z * kRowStep;
-            w[z] = *reinterpret_cast<const uint4*>(kt + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
-          }
+              reinterpret_cast<const int*>(smem + Lay::oR) + (st * Lay::kRows + (z * 32 >> a.shift)) * KD + ch * 8);
           const int4 u = rc[0], v = rc[1];
           const int d[8] = {ri[0] - u.x, ri[1] - u.y, ri[2] - u.z, ri[3] - u.w,
                             ri[4] - v.x, ri[5] - v.y, ri[6] - v.z, ri[7] - v.w};
           int most = d[0];
 #pragma unroll
           for (int e = 1; e < 8; ++e) most = max(most, d[e]);
-          // beyond the operands' range, on a key that some row sees
+          // beyond the operands' range, on a page that some row sees
           if (most > (int)kAnchorRange)
-            flag |= j0 + z0 * 32 < min(s.kv, s.pos0 + s.ni) && j0 + z0 * 32 + 32 > s.from;
-          __nv_bfloat162 f[4];
+            flag |= j0 + z * 32 < min(s.kv, s.pos0 + s.ni) && j0 + z * 32 + PS > s.from;
+          f0 = pow2_bf16(d[0]) | (pow2_bf16(d[1]) << 16);
+          f1 = pow2_bf16(d[2]) | (pow2_bf16(d[3]) << 16);
+          f2 = pow2_bf16(d[4]) | (pow2_bf16(d[5]) << 16);
+          f3 = pow2_bf16(d[6]) | (pow2_bf16(d[7]) << 16);
+        };
+        auto vec = [&](int z, int x) {  // this thread's x-th vector of rows [32 z, 32 z + 32)
+          const int r = z * 32 + rs + x * kRowStep;
+          return reinterpret_cast<uint4*>(kt + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+        };
+        auto load = [&](int z, uint4 (&w)[kBatch]) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t b = pow2_bf16(d[2 * e]) | (pow2_bf16(d[2 * e + 1]) << 16);
-            f[e] = *reinterpret_cast<const __nv_bfloat162*>(&b);
+          for (int x = 0; x < kBatch; ++x) w[x] = *vec(z, x);
+        };
+        auto scale = [&](int z, uint4 (&w)[kBatch]) {
+#pragma unroll
+          for (int x = 0; x < kBatch; ++x) {
+            *vec(z, x) = make_uint4(mul_bf16x2(w[x].x, f0), mul_bf16x2(w[x].y, f1),
+                                    mul_bf16x2(w[x].z, f2), mul_bf16x2(w[x].w, f3));
           }
-#pragma unroll
-          for (int z = 0; z < kBatch; ++z) {
-            const int r = z0 * 32 + rs + z * kRowStep;
-            __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&w[z]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = __hmul2(h[e], f[e]);
-            *reinterpret_cast<uint4*>(kt + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = w[z];
-          }
+        };
+        // a shared-memory load takes hundreds of cycles while the tensor core
+        // streams its operands: the next 32 rows are always in flight
+#pragma unroll 1
+        for (int z = 0; z < 4; ++z) {
+          uint4 wa[kBatch];
+          load(z, wa);
+          factors(z);
+          scale(z, wa);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_KREADY + st));
-        if (y < s.fa || y >= s.fb) {
-          const int vs = g % kVS;
-          if (!__all_sync(0xffffffffu, wait_bar(bar(B_VRAW + vs), (raw >> vs) & 1u, a.status, abort_flag))) {
-            ok = false;
-            break;
-          }
-          raw ^= 1u << vs;
-          const int nk = s.kv - j0;
-          uint8_t* vt = smem + Lay::oV + vs * Lay::kT + (ch / 8) * (BN * 128);
-          uint32_t bad = 0;
-#pragma unroll 4
-          for (int r = rs; r < BN; r += kRowStep) {
-            uint4* w = reinterpret_cast<uint4*>(vt + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
-            if (r >= nk) {
-              *w = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-              const uint4 x = *w;
-              bad |= not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w);
-            }
-          }
-          flag |= bad != 0;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_VFULL + vs));
+        // The value tile of two tiles ago, where it is partly masked: by now it
+        // has landed, and the keys that the next S need are scaled already.
+        if (nk2 >= 0 && !check_values(g - 2, nk2, unit2)) {
+          ok = false;
+          break;
         }
+        nk2 = nk1;
+        unit2 = unit1;
+        nk1 = y < s.fa || y >= s.fb ? max(0, min(BN, s.kv - j0)) : -1;
+        unit1 = s.place * a.HQ + s.h;
       }
-      if (flag) flags.set(s.place, s.h, a.HQ);
+      if (flag) flags.set(s.place * a.HQ + s.h, a.HQ);
+    }
+#pragma unroll 1
+    for (int left = 2; ok && left > 0; --left) {
+      if (nk2 >= 0) ok = check_values(g - left, nk2, unit2);
+      nk2 = nk1;
+      unit2 = unit1;
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -617,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool row_ok = r < s.ni;
       // a unit of few rows leaves whole warps without one: they keep step only
       const bool idle = quarter * 32 >= s.ni;
-      float m_use = -INFINITY, l = 0.f;
+      float m_use = -INFINITY, l = 0.f, raise = 0.f;
       const int first = (g0 + grp) & 1;       // this group's first tile of the segment
       for (int y = first; y < cnt; y += 2) {
         const int g = g0 + y;
@@ -632,120 +679,116 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const bool fast = y >= s.fa && y < s.fb;  // the same for the whole CTA
-        bool done = false;
-        // One pass when every row's running max is set: exponentials against
-        // it, kept in registers and stored only if no row's sum exceeds
-        // 2^threshold (then no term does; an overflow or NaN fails the test
-        // too); else the two passes below.
-        if (fast && __all_sync(0xffffffffu, !row_ok || m_use != -INFINITY)) {
-          uint32_t pk1[64];
-          float r0 = 0.f, r1 = 0.f;
-          const float off = -m_use;
-#pragma unroll
-          for (int cc = 0; cc < BN; cc += 64) {
-            uint32_t sv[64];
+        // The row's visible keys of the tile are [ja, jb), both rising from row
+        // to row.  Per 32 keys the whole warp decides whether all of its rows
+        // see all of them, none sees any, or it has to look at each.
+        const int dist = s.pos0 + r - (s.j0 + y * BN);  // from the tile's first key to the row
+        const int jb = dist + 1, ja = a.window > 0 ? jb - a.window : -BN;
+        const int last = min(31, s.ni - 1 - quarter * 32);  // the warp's last row
+        auto all_seen = [&](int cc) {
+          return fast || (cc >= ja - lane + last && cc + 32 <= jb - lane);
+        };
+        auto none_seen = [&](int cc) {
+          return !fast && (cc >= jb - lane + last || cc + 32 <= ja - lane);
+        };
+        // The exponentials are taken against a reference of the row's own, its
+        // max over the first keys that it sees; it need not be the max of all,
+        // since P (bf16), its sum and O (fp32) are floating point: it is raised,
+        // and O scaled, by whole powers of two when a tile's sum has passed
+        // 2^8, and a tile that passes 2^100 flags the unit.  So S is read once,
+        // and P can take its place 32 keys at a time.
+        if (__any_sync(0xffffffffu, row_ok && m_use == -INFINITY)) {
+          float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll 1
+          for (int cc = 0; cc < BN; cc += 32) {
+            if (none_seen(cc)) continue;
+            uint32_t sv[32];
             tmem_ld32(s_addr + cc, sv);
-            tmem_ld32(s_addr + cc + 32, sv + 32);
+            tmem_wait_ld();
+            if (all_seen(cc)) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                mx0 = fmaxf(mx0, __uint_as_float(sv[e]));
+                mx1 = fmaxf(mx1, __uint_as_float(sv[e + 1]));
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const bool vis = cc + e >= ja && cc + e < jb;
+                mx0 = fmaxf(mx0, vis ? __uint_as_float(sv[e]) : -INFINITY);
+              }
+            }
+          }
+          if (m_use == -INFINITY) m_use = fmaxf(mx0, mx1) * sl2;
+        }
+        if (__any_sync(0xffffffffu, raise != 0.f)) {
+          // (S of this tile came behind this group's last P V, so O is whole)
+          const float f = exp2f(-raise);
+#pragma unroll 1
+          for (int cc = 0; cc < V / 32; ++cc) {
+            uint32_t ov[32];
+            tmem_ld32(o_addr + cc * 32, ov);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
+            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
+            tmem_st32(o_addr + cc * 32, ov);
+          }
+          l *= f;
+          m_use += raise;
+        }
+        const float off = m_use == -INFINITY ? 0.f : -m_use;
+        float r0 = 0.f, r1 = 0.f;
+        if (fast) {
+#pragma unroll 1
+          for (int cc = 0; cc < BN; cc += 32) {
+            uint32_t sv[32], pk[16];
+            tmem_ld32(s_addr + cc, sv);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
               const float p0 = exp2f(fmaf(__uint_as_float(sv[e]), sl2, off));
               const float p1 = exp2f(fmaf(__uint_as_float(sv[e + 1]), sl2, off));
               const float p2 = exp2f(fmaf(__uint_as_float(sv[e + 2]), sl2, off));
               const float p3 = exp2f(fmaf(__uint_as_float(sv[e + 3]), sl2, off));
               r0 += p0 + p2;
               r1 += p1 + p3;
-              pk1[(cc + e) / 2] = pack_bf16x2(p0, p1);
-              pk1[(cc + e) / 2 + 1] = pack_bf16x2(p2, p3);
+              pk[e / 2] = pack_bf16x2(p0, p1);
+              pk[e / 2 + 1] = pack_bf16x2(p2, p3);
             }
+            tmem_st16(s_addr + cc / 2, pk);
           }
-          if (!__any_sync(0xffffffffu, row_ok && !(r0 + r1 <= kRescaleBound))) {
-#pragma unroll
-            for (int cc = 0; cc < 4; ++cc) tmem_st16(s_addr + cc * 16, pk1 + cc * 16);
-            tmem_wait_st();
-            l += r0 + r1;
-            done = true;
-          }
-        }
-        if (!done) {
-          // the row's visible keys of the tile: [ja, jb)
-          const int dist = s.pos0 + r - (s.j0 + y * BN);  // from the tile's first key to the row
-          const int jb = row_ok ? min(BN, dist + 1) : 0;
-          const int ja = a.window > 0 ? dist + 1 - a.window : 0;
-          // pass 1: row max
-          float mx0 = -INFINITY, mx1 = -INFINITY;
+        } else {
 #pragma unroll 1
           for (int cc = 0; cc < BN; cc += 32) {
-            uint32_t sv[32];
-            tmem_ld32(s_addr + cc, sv);
-            tmem_wait_ld();
-            if (fast) {
+            uint32_t pk[16];
+            if (none_seen(cc)) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) pk[e] = 0u;
+            } else {
+              uint32_t sv[32];
+              tmem_ld32(s_addr + cc, sv);
+              tmem_wait_ld();
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
-                mx0 = fmaxf(mx0, __uint_as_float(sv[e]) * sl2);
-                mx1 = fmaxf(mx1, __uint_as_float(sv[e + 1]) * sl2);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const bool vis = cc + e >= ja && cc + e < jb;
-                mx0 = fmaxf(mx0, vis ? __uint_as_float(sv[e]) * sl2 : -INFINITY);
-              }
-            }
-          }
-          const float mx = fmaxf(mx0, mx1);
-          const bool resc = mx > m_use + kRescaleThreshold;
-          const float m_new = resc ? mx : m_use;
-          const float alpha = m_use == -INFINITY ? 0.f : exp2f(m_use - m_new);
-          if (y > first) {
-            // this group's previous P V has landed in its O before O is rescaled
-            if (!__all_sync(0xffffffffu, wait_bar(bar(B_PVDONE + grp), ((g >> 1) - 1) & 1, a.status,
-                                                  abort_flag))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            if (__any_sync(0xffffffffu, resc)) {
-              const float f = resc ? alpha : 1.f;
-#pragma unroll 1
-              for (int cc = 0; cc < V / 32; ++cc) {
-                uint32_t ov[32];
-                tmem_ld32(o_addr + cc * 32, ov);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
-                tmem_st32(o_addr + cc * 32, ov);
-              }
-              tmem_wait_st();
-            }
-          }
-          if (resc) l *= alpha;
-          m_use = m_new;
-          const float m_eff = m_use == -INFINITY ? 0.f : m_use;
-          // pass 2: p = exp2(s - m), row sum, bf16 P over the consumed S columns
-          float rs0 = 0.f, rs1 = 0.f;
-#pragma unroll 1
-          for (int cc = 0; cc < BN; cc += 32) {
-            uint32_t sv[32];
-            tmem_ld32(s_addr + cc, sv);
-            tmem_wait_ld();
-            uint32_t pk2[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float p0 = exp2f(fmaf(__uint_as_float(sv[e]), sl2, -m_eff));
-              float p1 = exp2f(fmaf(__uint_as_float(sv[e + 1]), sl2, -m_eff));
-              if (!fast) {
+                float p0 = exp2f(fmaf(__uint_as_float(sv[e]), sl2, off));
+                float p1 = exp2f(fmaf(__uint_as_float(sv[e + 1]), sl2, off));
                 p0 = cc + e >= ja && cc + e < jb ? p0 : 0.f;
                 p1 = cc + e + 1 >= ja && cc + e + 1 < jb ? p1 : 0.f;
+                r0 += p0;
+                r1 += p1;
+                pk[e / 2] = pack_bf16x2(p0, p1);
               }
-              rs0 += p0;
-              rs1 += p1;
-              pk2[e / 2] = pack_bf16x2(p0, p1);
             }
-            tmem_st16(s_addr + cc / 2, pk2);
+            tmem_st16(s_addr + cc / 2, pk);
           }
-          tmem_wait_st();
-          l += rs0 + rs1;
+        }
+        tmem_wait_st();
+        r0 += r1;
+        l += r0;
+        raise = 0.f;
+        if (row_ok && !(r0 <= kRaiseAbove)) {
+          if (r0 <= kFlagAbove) raise = (float)((__float_as_int(r0) >> 23) - 127);
+          else flags.set(s.place * a.HQ + s.h, a.HQ);  // NaN too
         }
         tc_fence_before();
         __syncwarp();
@@ -889,7 +932,7 @@ __global__ void __launch_bounds__(256) chunk_queries_kernel(AttnArgs a, __nv_bfl
         wide |= fabsf(pv[e]) > kAnchorRange;
         qv[e] *= exp2f(pv[e]);
       }
-      if (wide) flags.set(flags.place(r, b), off / a.K, a.HQ);
+      if (wide) flags.set((int)flags.place(r, b) * a.HQ + off / a.K, a.HQ);
       store8(qh + (long)t * a.HQ * a.K + off, qv);
     }
   }

@@ -467,6 +467,30 @@ def test_attn_strong_decay(K, dt, decay):
     _attn_case(2, 1, K, K, 32, dt, [1, 150, 40], [90, 70, 0], decay=decay)
 
 
+@pytest.mark.parametrize("jump", [20.0, 300.0])
+def test_attn_scores_that_jump(jump):
+    """Scores that rise from tile to tile by far more than one reference serves
+    (300 units of log2: past what fp32 sums hold against it), and keys that
+    take the whole weight."""
+    x, cu, kv, table = _attn_inputs(2, 1, 128, 128, 64, BF, [150, 2], [500, 300], decay=0.0)
+    x["p"].zero_()
+    x["r_pages"].zero_()
+    for i, n in enumerate(kv):
+        for j in (60, 200, 330, 420, 610):
+            if j < n:
+                page, off = int(table[i, j // 64]), j % 64
+                # along the first query row: a score of about `jump` times its rank
+                d = x["q"][cu[i]].float()
+                x["k_pages"][page, :, off] = (d * (jump * j / 200.0 / 1.4427 / (128 ** -0.5))
+                                              / (d * d).sum(-1, keepdim=True)).to(BF)
+    o_ref, _ = ref.attn(x["q"], x["p"], cu, kv, torch.tensor(table), x["k_pages"], x["v_pages"],
+                        x["r_pages"], 64, 128 ** -0.5)
+    o = api.wall_paged_attn(x["q"], x["p"], _i32(cu), _i32(kv), _i32(table), x["k_pages"],
+                            x["v_pages"], x["r_pages"])
+    _status_ok()
+    assert_fwd(BF, o, o_ref)
+
+
 def test_attn_far_positions_are_exact():
     """Prefixes of millions of powers of two: only differences matter, to the
     last bit."""
