@@ -78,8 +78,9 @@ int wall_paged_release(const int32_t* finished, int32_t* lens, int32_t* block_ta
 size_t wall_paged_append_workspace(int n_req, int n_tokens, int max_new, int HQ, int K,
                                    int page_size) {
   const int shift = page_shift(page_size);
-  if (shift < 0 || n_req < 1 || n_tokens < 1 || HQ < 1 || K < 1) return 0;
-  return paged_append_ws(n_req, n_tokens, HQ, K, shift, max_new);
+  if (shift < 0 || n_req < 1 || n_tokens < 1 || HQ < 1 || K < 1 || max_new < 0) return 0;
+  return paged_append_ws(n_req, n_tokens, HQ, K, shift,
+                         max_new > 0 && max_new < n_tokens ? max_new : n_tokens);
 }
 
 int wall_paged_append(const void* k, const void* v, const void* g, int dtype, const int32_t* cu_q,
@@ -109,7 +110,7 @@ int wall_paged_append(const void* k, const void* v, const void* g, int dtype, co
   pb.NP = num_pages;
   pb.k_pages = k_pages; pb.v_pages = v_pages; pb.r_pages = r_pages;
   pb.carry_in = carry_in; pb.carry_out = carry_out; pb.p = p;
-  const size_t need = paged_append_ws(n_req, n_tokens, HQ, K, pb.shift, max_new);
+  const size_t need = paged_append_ws(n_req, n_tokens, HQ, K, pb.shift, pb.max_new);
   if (need > 0 && (workspace_bytes < need || !ok_ptr(workspace, 16))) return WALL_ERR_INVALID_ARG;
   return paged_append(pb, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
