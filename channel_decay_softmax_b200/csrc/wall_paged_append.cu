@@ -26,9 +26,14 @@ namespace {
 
 using namespace paged;
 
-constexpr int kSlab = 128;  // channels of a CTA: four a lane
-constexpr int kWarps = 8;   // of a CTA that takes one token a request
-constexpr int W = 16;       // of one that takes a block of RL positions, RL / W tokens each
+constexpr int kWarps = 8;   // of a CTA
+constexpr int kOneSlab = 128;  // one token a request: a warp's channels, four a lane
+// Blocks of RL positions: a CTA takes 64 channels, sixteen half-warps of RL / 16
+// tokens each, four channels a lane.  (CTAs of 128 channels and 512 threads
+// keep the same threads resident in half as many CTAs, whose barriers then
+// leave the SM idle: 40 against NN us.)
+constexpr int kSlab = 64;
+constexpr int W = 16;
 
 struct AppendArgs {
   const void *k, *v, *g;
@@ -87,9 +92,6 @@ struct Quad<__nv_bfloat16> {
     u = *reinterpret_cast<const uint2*>(x);
   }
   __device__ __forceinline__ void zero() { u = make_uint2(0u, 0u); }
-  // to the compiler a new value: what was computed from it is not kept in
-  // registers but computed again
-  __device__ __forceinline__ void renew() { asm volatile("" : "+r"(u.x), "+r"(u.y)); }
   __device__ __forceinline__ void get(float* f) const {
     f[0] = __uint_as_float(u.x << 16);
     f[1] = __uint_as_float(u.x & 0xffff0000u);
@@ -107,9 +109,6 @@ struct Quad<float> {
   float4 u;
   __device__ __forceinline__ void load(const float* x) { u = *reinterpret_cast<const float4*>(x); }
   __device__ __forceinline__ void zero() { u = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void renew() {
-    asm volatile("" : "+f"(u.x), "+f"(u.y), "+f"(u.z), "+f"(u.w));
-  }
   __device__ __forceinline__ void get(float* f) const {
     f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
   }
@@ -118,17 +117,25 @@ struct Quad<float> {
   }
 };
 
-// p of a token and the factor 2^-p of its key row from its prefix and its
-// page's anchor.  A prefix that left the page's range is reported (the row
-// would leave the numbers that bf16 has); a NaN gate makes both NaN.
-__device__ __forceinline__ void token_factor(long long P, int R, float g, float& p, float& f,
-                                             bool& wide) {
-  const long long d = P - ((long long)R << kFrac);
-  const int lo = (int)d;
-  p = __int2float_rn(lo) * kStep;
-  wide |= d != (long long)lo || fabsf(p) > kPageRange;
-  if (g != g) p = g;
-  f = exp2f(-p);
+// The prefix beyond the page's anchor, in 32 bits from token to token: inside a
+// page's range it fits with room to spare.  (Before a page's first token it
+// need not, and is then right modulo 2^32, as the token's own value is small.)
+// What leaves the range is reported: a step that overflows (`lost` < 0), or a
+// value past it.
+__device__ __forceinline__ int from_anchor(long long P, int R) {
+  return (int)(P - ((long long)R << kFrac));
+}
+__device__ __forceinline__ int add_step(int d, int e, int& lost) {
+  const int s = (int)((unsigned)d + (unsigned)e);
+  lost |= (d ^ s) & (e ^ s);
+  return s;
+}
+// p of a token, and whether it leaves the range that the key row 2^-p k stays a
+// number in.
+__device__ __forceinline__ float token_prefix(int d, bool& wide) {
+  const float p = __int2float_rn(d) * kStep;
+  wide |= fabsf(p) > kPageRange;
+  return p;
 }
 
 // A slot as the pool's position (below 2^31), or -1 (reported) where it lies
@@ -172,15 +179,22 @@ __device__ __forceinline__ void load_tokens(const T* p, int stride, int xa, int 
     if (x >= xa && x < xb && live) q[x].load(p + x * stride);
   }
 }
+// The tokens' gate steps and their sums; `nan`: some gate is none.
 template <typename T, int TPW>
-__device__ __forceinline__ void gate_sums(const Quad<T> (&g)[TPW], long long* out) {
+__device__ __forceinline__ void gate_steps(const Quad<T> (&g)[TPW], int (&step)[TPW][4],
+                                           long long* out, bool& nan) {
   long long sum[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int x = 0; x < TPW; ++x) {
     float f[4];
     g[x].get(f);
+    const float t = (f[0] + f[1]) + (f[2] + f[3]);
+    nan |= t != t;  // (or infinities of both signs: looked at again)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] += gate_fixed(f[e]);
+    for (int e = 0; e < 4; ++e) {
+      step[x][e] = gate_fixed(f[e]);
+      sum[e] += step[x][e];
+    }
   }
   longlong2* o = reinterpret_cast<longlong2*>(out);
   o[0] = make_longlong2(sum[0], sum[1]);
@@ -198,11 +212,12 @@ __device__ __forceinline__ void store4(long long* p, const long long (&x)[4]) {
 
 // Blocks of RL positions, a page or several.  kRuns: the CTA takes one run, from its prefix; else all blocks of request blockIdx.x.
 template <typename T, int RL, bool kRuns>
-__global__ void __launch_bounds__(W * 32, RL == 64 && sizeof(T) == 2 ? 2 : 1) append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, RL == 64 && sizeof(T) == 2 ? 4 : 2)
+    append_kernel(AppendArgs a) {
   constexpr int TPW = RL / W;
-  __shared__ __align__(16) long long s_sum[W][kSlab];  // the warps' sums, then their prefixes
-  __shared__ __align__(16) int s_R[RL / 32][kSlab];    // anchors of the pages that begin in the block
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ __align__(16) long long s_sum[W][kSlab];  // the groups' sums, then their prefixes
+  __shared__ __align__(16) int s_first[RL / 32][kSlab];  // gate steps of the tokens that begin pages
+  const int lane = threadIdx.x & 15, grp = threadIdx.x >> 4;
   int i, t0, n, kv, base;
   bool none;
   if constexpr (kRuns) {
@@ -229,7 +244,7 @@ __global__ void __launch_bounds__(W * 32, RL == 64 && sizeof(T) == 2 ? 2 : 1) ap
   const int h = live ? c / a.K : 0, ch = live ? c - h * a.K : 0;
   const int PS1 = (1 << a.shift) - 1;
   if (none) {
-    if (live && warp == 0 && a.carry_out != a.carry_in) {
+    if (live && grp == 0 && a.carry_out != a.carry_in) {
       long long x[4];
       load4(a.carry_in + (long)i * C + c, x);
       store4(a.carry_out + (long)i * C + c, x);
@@ -247,9 +262,10 @@ __global__ void __launch_bounds__(W * 32, RL == 64 && sizeof(T) == 2 ? 2 : 1) ap
     carry = kRuns ? a.runs[(long)blockIdx.x * C + sc] : a.carry_in[(long)i * C + sc];
   bool wide = false, bad = false;
   for (;; base += RL) {
-    const int o0 = base + warp * TPW;  // this warp's first position
+    const int o0 = base + grp * TPW;  // this group's first position
     const int xa = max(0, ctx - o0), xb = min(TPW, kv - o0);  // its tokens [xa, xb)
     const int tw = t0 + o0 - ctx;  // their place among the packed rows (below 0 before the first)
+    const int po = o0 & ~PS1;      // its page: TPW divides a page
     Quad<T> gq[TPW], kq[TPW];
     load_tokens(g + (long)tw * C, C, xa, xb, live, gq);
     load_tokens(k + (long)tw * a.H * a.K, a.H * a.K, xa, xb, live, kq);
@@ -257,9 +273,21 @@ __global__ void __launch_bounds__(W * 32, RL == 64 && sizeof(T) == 2 ? 2 : 1) ap
 #pragma unroll
     for (int x = 0; x < TPW; ++x)
       row[x] = x >= xa && x < xb ? slot_row(a.slots[tw + x], a, bad) : -1;
-    gate_sums(gq, &s_sum[warp][lane * 4]);
+    // a page begun by an earlier call: its anchor stands in the pool
+    int4 R = make_int4(0, 0, 0, 0);
+    if (xa < xb && po < ctx) {
+      int first = -1;
 #pragma unroll
-    for (int x = 0; x < TPW; ++x) gq[x].renew();
+      for (int x = TPW - 1; x >= 0; --x) first = x >= xa && x < xb ? row[x] : first;
+      if (first >= 0 && live)
+        R = *reinterpret_cast<const int4*>(a.rp + (long)(first >> a.shift) * C + c);
+    }
+    int step[TPW][4];
+    bool nan = false;
+    gate_steps(gq, step, &s_sum[grp][lane * 4], nan);
+    if (po == o0)
+      *reinterpret_cast<int4*>(&s_first[(o0 - base) >> 5][lane * 4]) =
+          make_int4(step[0][0], step[0][1], step[0][2], step[0][3]);
     __syncthreads();
     if (threadIdx.x < kSlab) {
 #pragma unroll 4
@@ -271,49 +299,45 @@ __global__ void __launch_bounds__(W * 32, RL == 64 && sizeof(T) == 2 ? 2 : 1) ap
     }
     __syncthreads();
     long long P[4];
-    load4(&s_sum[warp][lane * 4], P);
-    int4 R = make_int4(0, 0, 0, 0);
-    const int po = o0 & ~PS1;  // this warp's page: TPW divides a page
-    // a page that begins here, at a token of this call
-    if (po == o0 && xa == 0 && xb > 0) {
-      float f[4];
-      gq[0].get(f);
-      R = make_int4(page_anchor(P[0] + gate_fixed(f[0])), page_anchor(P[1] + gate_fixed(f[1])),
-                    page_anchor(P[2] + gate_fixed(f[2])), page_anchor(P[3] + gate_fixed(f[3])));
-      *reinterpret_cast<int4*>(&s_R[(o0 - base) >> 5][lane * 4]) = R;
-      if (row[0] >= 0 && live) *reinterpret_cast<int4*>(a.rp + (long)(row[0] >> a.shift) * C + c) = R;
+    if (xa < xb && po >= ctx) {  // a page that begins here, at a token of this call
+      load4(&s_sum[(po - base) / TPW][lane * 4], P);
+      const int4 e = *reinterpret_cast<const int4*>(&s_first[(po - base) >> 5][lane * 4]);
+      R = make_int4(page_anchor(P[0] + e.x), page_anchor(P[1] + e.y), page_anchor(P[2] + e.z),
+                    page_anchor(P[3] + e.w));
+      if (po == o0 && row[0] >= 0 && live)
+        *reinterpret_cast<int4*>(a.rp + (long)(row[0] >> a.shift) * C + c) = R;
     }
-    __syncthreads();
-    if (xa < xb) {
-      if (po >= ctx) {
-        R = *reinterpret_cast<const int4*>(&s_R[(po - base) >> 5][lane * 4]);
-      } else {
-        // begun by an earlier call: its anchor stands in the pool
-        int first = -1;
-#pragma unroll
-        for (int x = TPW - 1; x >= 0; --x) first = x >= xa && x < xb ? row[x] : first;
-        if (first >= 0 && live)
-          R = *reinterpret_cast<const int4*>(a.rp + (long)(first >> a.shift) * C + c);
-      }
-    }
-    const int Rv[4] = {R.x, R.y, R.z, R.w};
+    load4(&s_sum[grp][lane * 4], P);
+    int d[4] = {from_anchor(P[0], R.x), from_anchor(P[1], R.y), from_anchor(P[2], R.z),
+                from_anchor(P[3], R.w)};
     float* pw = a.p + (long)tw * C + c;
+    int lost = 0;
 #pragma unroll
     for (int x = 0; x < TPW; ++x) {
       if (x < xa || x >= xb || !live) continue;
-      float f[4], kf[4], pv[4], fac;
-      gq[x].get(f);
+      float kf[4], pv[4];
       kq[x].get(kf);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        P[e] += gate_fixed(f[e]);
-        token_factor(P[e], Rv[e], f[e], pv[e], fac, wide);
-        kf[e] *= fac;
+        d[e] = add_step(d[e], step[x][e], lost);
+        pv[e] = token_prefix(d[e], wide);
       }
+      if (x == 0 && po == o0) lost = 0;  // the page's first token
+      if (nan) {  // a NaN gate makes its token's p and key row NaN
+        float f[4];
+        Quad<T> gx;
+        gx.load(g + ((long)tw + x) * C);
+        gx.get(f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pv[e] = f[e] != f[e] ? f[e] : pv[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) kf[e] *= exp2f(-pv[e]);
       *reinterpret_cast<float4*>(pw + x * C) = make_float4(pv[0], pv[1], pv[2], pv[3]);
       if (row[x] >= 0)
         Quad<T>::store(kp + ((((long)(row[x] >> a.shift) * a.HQ + h) << a.shift) + (row[x] & PS1)) * a.K, kf);
     }
+    wide |= lost < 0;
     if (kRuns || base + RL >= kv) break;
     __syncthreads();  // the prefixes have been read
   }
@@ -322,21 +346,23 @@ __global__ void __launch_bounds__(W * 32, RL == 64 && sizeof(T) == 2 ? 2 : 1) ap
   if (bad) record_status(a.status, WALL_ERR_INVALID_ARG);
 }
 
-// Each run's sum of gate steps, a CTA per (run, 128 channels).
+// Each run's sum of gate steps, a CTA per (run, 64 channels).
 template <typename T, int RL>
-__global__ void __launch_bounds__(W * 32) run_sums_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kWarps * 32) run_sums_kernel(AppendArgs a) {
   constexpr int TPW = RL / W;
   __shared__ __align__(16) long long s_sum[W][kSlab];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 15, grp = threadIdx.x >> 4;
   const Run<RL> r = run_at<RL>(a.bt, blockIdx.x);
   if (r.i < 0 || r.none) return;
   const int C = a.HQ * a.K;
   const int c = blockIdx.y * kSlab + lane * 4;
-  const int o0 = r.base + warp * TPW;
+  const int o0 = r.base + grp * TPW;
   const int xa = max(0, r.ctx - o0), xb = min(TPW, r.kv - o0);
   Quad<T> gq[TPW];
   load_tokens(static_cast<const T*>(a.g) + ((long)r.t0 + o0 - r.ctx) * C + c, C, xa, xb, c < C, gq);
-  gate_sums(gq, &s_sum[warp][lane * 4]);
+  int step[TPW][4];
+  bool nan = false;
+  gate_steps(gq, step, &s_sum[grp][lane * 4], nan);
   __syncthreads();
   const int x = threadIdx.x;
   if (x < kSlab && blockIdx.y * kSlab + x < C) {
@@ -404,7 +430,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_one_kernel(AppendArgs a, i
         *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + (long)t * a.H * a.V + ch);
     return;
   }
-  const int C = a.HQ * a.K, c = slab * kSlab + lane * 4;
+  const int C = a.HQ * a.K, c = slab * kOneSlab + lane * 4;
   if (c >= C) return;
   const int h = c / a.K, ch = c - h * a.K;
   longlong2 u = make_longlong2(0, 0), v = u;
@@ -427,11 +453,13 @@ __global__ void __launch_bounds__(kWarps * 32) append_one_kernel(AppendArgs a, i
   float f[4], kf[4], pv[4];
   gq.get(f);
   kq.get(kf);
-  const long long P[4] = {u.x + gate_fixed(f[0]), u.y + gate_fixed(f[1]), v.x + gate_fixed(f[2]),
-                          v.y + gate_fixed(f[3])};
+  const int step[4] = {gate_fixed(f[0]), gate_fixed(f[1]), gate_fixed(f[2]), gate_fixed(f[3])};
+  const long long before[4] = {u.x, u.y, v.x, v.y};
+  const long long P[4] = {u.x + step[0], u.y + step[1], v.x + step[2], v.y + step[3]};
+  const bool begins = ((kv - n) & PS1) == 0;  // the token begins its page
   int4 r4 = make_int4(0, 0, 0, 0);
   int4* rp = reinterpret_cast<int4*>(a.rp + (long)page * C + c);
-  if (((kv - n) & PS1) == 0) {  // it begins its page
+  if (begins) {
     r4 = make_int4(page_anchor(P[0]), page_anchor(P[1]), page_anchor(P[2]), page_anchor(P[3]));
     if (!bad) *rp = r4;
   } else if (!bad) {
@@ -441,9 +469,11 @@ __global__ void __launch_bounds__(kWarps * 32) append_one_kernel(AppendArgs a, i
   bool wide = false;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    float fac;
-    token_factor(P[e], R[e], f[e], pv[e], fac, wide);
-    kf[e] *= fac;
+    int lost = 0;
+    pv[e] = token_prefix(add_step(from_anchor(before[e], R[e]), step[e], lost), wide);
+    wide |= !begins && lost < 0;
+    if (f[e] != f[e]) pv[e] = f[e];
+    kf[e] *= exp2f(-pv[e]);
   }
   *reinterpret_cast<float4*>(a.p + (long)t * C + c) = make_float4(pv[0], pv[1], pv[2], pv[3]);
   if (!bad)
@@ -467,12 +497,12 @@ template <typename T, int RL>
 int append_tokens(AppendArgs& a, int max_new, int v_slabs, cudaStream_t stream) {
   const int slabs = a.k_slabs + v_slabs;
   if (blocks_of(max_new, a.shift) <= kWalkBlocks) {
-    append_kernel<T, RL, false><<<dim3(a.bt.N, slabs), W * 32, 0, stream>>>(a);
+    append_kernel<T, RL, false><<<dim3(a.bt.N, slabs), kWarps * 32, 0, stream>>>(a);
   } else {
     const int places = (int)run_places(a.bt.N, a.bt.T, a.shift);
-    run_sums_kernel<T, RL><<<dim3(places, a.k_slabs), W * 32, 0, stream>>>(a);
+    run_sums_kernel<T, RL><<<dim3(places, a.k_slabs), kWarps * 32, 0, stream>>>(a);
     run_scan_kernel<RL><<<dim3(a.bt.N, ceil_div((long)a.HQ * a.K, 32)), 256, 0, stream>>>(a);
-    append_kernel<T, RL, true><<<dim3(places, slabs), W * 32, 0, stream>>>(a);
+    append_kernel<T, RL, true><<<dim3(places, slabs), kWarps * 32, 0, stream>>>(a);
   }
   return cudaGetLastError() == cudaSuccess ? WALL_OK : WALL_ERR_CUDA;
 }
@@ -481,6 +511,7 @@ template <typename T>
 int append(AppendArgs& a, int max_new, cudaStream_t stream) {
   const int v_slabs = ceil_div((long)a.H * a.V * sizeof(T), 32 * 16);
   if (max_new == 1) {
+    a.k_slabs = ceil_div((long)a.HQ * a.K, kOneSlab);
     const long warps = (long)a.bt.N * (a.k_slabs + v_slabs);
     append_one_kernel<T><<<ceil_div(warps, kWarps), kWarps * 32, 0, stream>>>(a, v_slabs);
     return cudaGetLastError() == cudaSuccess ? WALL_OK : WALL_ERR_CUDA;

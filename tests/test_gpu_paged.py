@@ -301,6 +301,20 @@ def test_append_special_gates():
     g[20, 0, 0] = float("-inf")
     call(g)
     assert L.wall_get_status() == L.WALL_ERR_RANGE
+    # the same as the only new token of a call: the range is left in one step
+    # that passes 32 bits, too
+    for first in (0.0, -50.0):
+        pools = dict(k_pages=torch.zeros(2, HQ, PS, K, dtype=F32, device=DEV),
+                     v_pages=torch.zeros(2, H, PS, K, dtype=F32, device=DEV),
+                     r_pages=torch.zeros(2, HQ, K, dtype=torch.int32, device=DEV))
+        carry = torch.zeros(1, HQ, K, dtype=torch.int64, device=DEV)
+        one = torch.ones(1, H, K, device=DEV)
+        for n, step in enumerate((0.0, first, float("-inf"))):
+            assert L.wall_get_status() == L.WALL_OK
+            api.wall_paged_append(one, one, torch.full((1, HQ, K), step, device=DEV), _i32([0, 1]),
+                                  _i32([n + 1]), torch.tensor([n], device=DEV), carry=carry,
+                                  max_new=1, **pools)
+        assert L.wall_get_status() == L.WALL_ERR_RANGE
     slots = torch.arange(40, device=DEV)
     slots[3], slots[35] = -1, 4 * PS
     p, pools, carry = call(torch.zeros(40, HQ, K, device=DEV), slots)
