@@ -6,6 +6,7 @@ fallback.  If the library or a CUDA device is missing, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -279,31 +280,47 @@ def wall_attn_fwd_gate(q, k, v, g, B, T, H, HQ, K, V, scale, g_scalar, sink_bias
         _p(lse), _p(workspace), ws_bytes, _stream(stream)))
 
 
-# The paged calls run on the device that holds their tensors, whatever the
-# current one, on that device's current stream unless one is given.
-def _on_device(t, fn, *args, stream=None):
-    if t.device.index == torch.cuda.current_device():
-        return fn(*args, _stream(stream))
-    with torch.cuda.device(t.device):
-        return fn(*args, _stream(stream))
+# The paged calls serve steps of a few microseconds: sizes come from the tensors
+# that api.py has checked, workspace sizes are computed once a shape, and the
+# call is made on the device that holds its tensors, on that device's current
+# stream unless one is given.
+
+def _raw_stream(index):
+    """The current stream's handle on a device (without a Stream object)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _on_device(name, fn, t, *args, stream=None):
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("libwall takes CUDA tensors")
+    s = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == torch._C._cuda_getDevice():
+        code = fn(*args, s)
+    else:
+        with torch.cuda.device(index):
+            code = fn(*args, s)
+    if code != WALL_OK:
+        raise WallError(name, code)
 
 
 def wall_paged_plan(new_lens, lens, block_table, free_list, free_count, n_req, max_pages,
                     num_pages, page_size, n_tokens, cu_q, kv_lens, slot_map, admitted, lens_out,
                     free_count_out, stream=None):
-    _check("wall_paged_plan", _on_device(
-        cu_q, lib().wall_paged_plan, _p(new_lens), _p(lens), _p(block_table), _p(free_list),
-        _p(free_count), n_req, max_pages, num_pages, page_size, n_tokens, _p(cu_q), _p(kv_lens),
-        _p(slot_map), _p(admitted), _p(lens_out), _p(free_count_out), stream=stream))
+    _on_device("wall_paged_plan", lib().wall_paged_plan, cu_q, _p(new_lens), _p(lens),
+               _p(block_table), _p(free_list), _p(free_count), n_req, max_pages, num_pages,
+               page_size, n_tokens, _p(cu_q), _p(kv_lens), _p(slot_map), _p(admitted),
+               _p(lens_out), _p(free_count_out), stream=stream)
 
 
 def wall_paged_release(finished, lens, block_table, free_list, free_count, n_req, max_pages,
                        num_pages, page_size, stream=None):
-    _check("wall_paged_release", _on_device(
-        free_list, lib().wall_paged_release, _p(finished), _p(lens), _p(block_table),
-        _p(free_list), _p(free_count), n_req, max_pages, num_pages, page_size, stream=stream))
+    _on_device("wall_paged_release", lib().wall_paged_release, free_list, _p(finished), _p(lens),
+               _p(block_table), _p(free_list), _p(free_count), n_req, max_pages, num_pages,
+               page_size, stream=stream)
 
 
+@functools.lru_cache(maxsize=4096)
 def wall_paged_append_workspace(n_req, n_tokens, max_new, HQ, K, page_size) -> int:
     return lib().wall_paged_append_workspace(n_req, n_tokens, max_new, HQ, K, page_size)
 
@@ -311,14 +328,15 @@ def wall_paged_append_workspace(n_req, n_tokens, max_new, HQ, K, page_size) -> i
 def wall_paged_append(k, v, g, cu_q, kv_lens, slot_map, n_req, n_tokens, max_new, H, HQ, K, V,
                       page_size, num_pages, k_pages, v_pages, r_pages, carry_in, carry_out, p,
                       workspace=None, stream=None):
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check("wall_paged_append", _on_device(
-        k_pages, lib().wall_paged_append, _p(k), _p(v), _p(g), dtype_code(k_pages.dtype),
-        _p(cu_q), _p(kv_lens), _p(slot_map), n_req, n_tokens, max_new, H, HQ, K, V, page_size,
-        num_pages, _p(k_pages), _p(v_pages), _p(r_pages), _p(carry_in), _p(carry_out), _p(p),
-        _p(workspace), ws_bytes, stream=stream))
+    ws_bytes = workspace.nbytes if workspace is not None else 0
+    _on_device("wall_paged_append", lib().wall_paged_append, k_pages, _p(k), _p(v), _p(g),
+               dtype_code(k_pages.dtype), _p(cu_q), _p(kv_lens), _p(slot_map), n_req, n_tokens,
+               max_new, H, HQ, K, V, page_size, num_pages, _p(k_pages), _p(v_pages),
+               _p(r_pages), _p(carry_in), _p(carry_out), _p(p), _p(workspace), ws_bytes,
+               stream=stream)
 
 
+@functools.lru_cache(maxsize=4096)
 def wall_paged_attn_workspace(dtype, n_req, n_tokens, max_new, H, HQ, K, V) -> int:
     return lib().wall_paged_attn_workspace(dtype_code(dtype), n_req, n_tokens, max_new, H, HQ, K,
                                            V)
@@ -328,9 +346,9 @@ def wall_paged_attn(q, p, cu_q, kv_lens, block_table, n_req, n_tokens, max_new, 
                     K, V, page_size, num_pages, k_pages, v_pages, r_pages, sink_bias, scale,
                     window_size, o, lse, workspace, stream=None):
     """New tokens' attention over the paged cache."""
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check("wall_paged_attn", _on_device(
-        k_pages, lib().wall_paged_attn, _p(q), _p(p), dtype_code(k_pages.dtype), _p(cu_q),
-        _p(kv_lens), _p(block_table), n_req, n_tokens, max_new, max_pages, H, HQ, K, V, page_size,
-        num_pages, _p(k_pages), _p(v_pages), _p(r_pages), _p(sink_bias), float(scale),
-        int(window_size), _p(o), _p(lse), _p(workspace), ws_bytes, stream=stream))
+    ws_bytes = workspace.nbytes if workspace is not None else 0
+    _on_device("wall_paged_attn", lib().wall_paged_attn, k_pages, _p(q), _p(p),
+               dtype_code(k_pages.dtype), _p(cu_q), _p(kv_lens), _p(block_table), n_req,
+               n_tokens, max_new, max_pages, H, HQ, K, V, page_size, num_pages, _p(k_pages),
+               _p(v_pages), _p(r_pages), _p(sink_bias), float(scale), int(window_size), _p(o),
+               _p(lse), _p(workspace), ws_bytes, stream=stream)

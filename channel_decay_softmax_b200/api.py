@@ -478,6 +478,15 @@ class WallDecodeCache:
 PAGE_SIZES = (32, 64, 128)
 
 
+def _are(device, *checks):
+    """Whether every (tensor, shape, dtype) holds and lies on the device: the
+    common case in one pass; the callers name what is wrong when it does not."""
+    for t, shape, dtype in checks:
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+            return False
+    return True
+
+
 class WallPagedPlan(NamedTuple):
     """Where a step's tokens go: row offsets cu_q [N+1] and kv_lens [N]
     (cached tokens after the step, 0 for a request that was refused), int32;
@@ -499,13 +508,15 @@ def _tables(lens, block_table, free_list, free_count):
     """Shapes of the page bookkeeping; returns (N, max_pages, num_pages)."""
     if lens.dim() != 1 or block_table.dim() != 2 or free_list.dim() != 1:
         raise ValueError("lens must be [N], block_table [N, max_pages], free_list [num_pages]")
-    N, MP = lens.shape[0], block_table.shape[1]
-    _expect("lens", lens, (N,), torch.int32)
-    _expect("block_table", block_table, (N, MP), torch.int32)
-    _expect("free_list", free_list, (free_list.shape[0],), torch.int32)
-    _expect("free_count", free_count, (1,), torch.int32)
-    _same_device(lens, block_table, free_list, free_count)
-    return N, MP, free_list.shape[0]
+    N, MP, NP = lens.shape[0], block_table.shape[1], free_list.shape[0]
+    if not _are(lens.get_device(), (lens, (N,), torch.int32), (block_table, (N, MP), torch.int32),
+                (free_list, (NP,), torch.int32), (free_count, (1,), torch.int32)):
+        _expect("lens", lens, (N,), torch.int32)
+        _expect("block_table", block_table, (N, MP), torch.int32)
+        _expect("free_list", free_list, (NP,), torch.int32)
+        _expect("free_count", free_count, (1,), torch.int32)
+        _same_device(lens, block_table, free_list, free_count)
+    return N, MP, NP
 
 
 def wall_paged_plan(new_lens, lens, block_table, free_list, free_count, page_size, n_tokens,
@@ -525,17 +536,16 @@ def wall_paged_plan(new_lens, lens, block_table, free_list, free_count, page_siz
     n_tokens = int(n_tokens)
     if n_tokens < 0 or MP < 1 or NP < 1:
         raise ValueError("need n_tokens >= 0, a block table of at least one page and a pool")
-    _expect("new_lens", new_lens, (N,), torch.int32)
     lens_out = lens if lens_out is None else lens_out
     free_count_out = free_count if free_count_out is None else free_count_out
-    _expect("lens_out", lens_out, (N,), torch.int32)
-    _expect("free_count_out", free_count_out, (1,), torch.int32)
-    _same_device(lens, new_lens, lens_out, free_count_out)
-    dev = lens.device
-    cu_q = torch.empty(N + 1, dtype=torch.int32, device=dev)
-    kv_lens = torch.empty(N, dtype=torch.int32, device=dev)
-    slot_map = torch.empty(n_tokens, dtype=torch.int64, device=dev)
-    admitted = torch.empty(N, dtype=torch.int32, device=dev)
+    if not _are(lens.get_device(), (new_lens, (N,), torch.int32), (lens_out, (N,), torch.int32),
+                (free_count_out, (1,), torch.int32)):
+        _expect("new_lens", new_lens, (N,), torch.int32)
+        _expect("lens_out", lens_out, (N,), torch.int32)
+        _expect("free_count_out", free_count_out, (1,), torch.int32)
+        _same_device(lens, new_lens, lens_out, free_count_out)
+    cu_q, kv_lens, admitted = lens.new_empty(3 * N + 1).split((N + 1, N, N))
+    slot_map = lens.new_empty(n_tokens, dtype=torch.int64)
     L.wall_paged_plan(new_lens, lens, block_table, free_list, free_count, N, MP, NP, PS, n_tokens,
                       cu_q, kv_lens, slot_map, admitted, lens_out, free_count_out)
     return WallPagedPlan(cu_q, kv_lens, slot_map, admitted)
@@ -559,14 +569,17 @@ def _pools(k_pages, v_pages, r_pages):
         raise ValueError("k_pages must be [num_pages, HQ, page_size, K] and v_pages "
                          "[num_pages, H, page_size, V]")
     NP, HQ, PS, K = k_pages.shape
-    H, V = v_pages.shape[1], v_pages.shape[3]
+    NPv, H, PSv, V = v_pages.shape
     _page_size(PS)
-    _io_dtype(k_pages, v_pages)
-    if v_pages.shape[0] != NP or v_pages.shape[2] != PS or H < 1 or HQ % H != 0:
+    _io_dtype(k_pages)
+    if NPv != NP or PSv != PS or H < 1 or HQ % H != 0:
         raise ValueError("v_pages must be [num_pages, H, page_size, V] with k_pages' pages and "
                          "HQ % H == 0")
-    _expect("r_pages", r_pages, (NP, HQ, K), torch.int32)
-    _same_device(k_pages, v_pages, r_pages)
+    if not _are(k_pages.get_device(), (v_pages, (NP, H, PS, V), k_pages.dtype),
+                (r_pages, (NP, HQ, K), torch.int32)):
+        _io_dtype(k_pages, v_pages)
+        _expect("r_pages", r_pages, (NP, HQ, K), torch.int32)
+        _same_device(k_pages, v_pages, r_pages)
     return NP, PS, H, HQ, K, V
 
 
@@ -575,8 +588,6 @@ def _batch(cu_q, kv_lens, max_new, T):
     if kv_lens.dim() != 1:
         raise ValueError("kv_lens must be [N]")
     N = kv_lens.shape[0]
-    _expect("kv_lens", kv_lens, (N,), torch.int32)
-    _expect("cu_q", cu_q, (N + 1,), torch.int32)
     max_new = T if max_new is None else int(max_new)
     if max_new < 1 and T > 0:
         raise ValueError("max_new must be positive")
@@ -599,19 +610,26 @@ def wall_paged_append(k, v, g, cu_q, kv_lens, slot_map, k_pages, v_pages, r_page
     if k.dim() != 3:
         raise ValueError("k must be [T, H, K]")
     T = k.shape[0]
-    _io_dtype(k_pages, k, v, g)
-    _expect("k", k, (T, H, K))
-    _expect("v", v, (T, H, V))
-    _expect("g", g, (T, HQ, K))
-    _expect("slot_map", slot_map, (T,), torch.int64)
     N, max_new = _batch(cu_q, kv_lens, max_new, T)
     carry_out = carry if carry_out is None else carry_out
-    _expect("carry", carry, (N, HQ, K), torch.int64)
-    _expect("carry_out", carry_out, (N, HQ, K), torch.int64)
-    _same_device(k_pages, k, v, g, cu_q, kv_lens, slot_map, carry, carry_out)
-    p = torch.empty((T, HQ, K), dtype=torch.float32, device=k_pages.device)
+    dt = k_pages.dtype
+    if not _are(k_pages.get_device(), (k, (T, H, K), dt), (v, (T, H, V), dt), (g, (T, HQ, K), dt),
+                (cu_q, (N + 1,), torch.int32), (kv_lens, (N,), torch.int32),
+                (slot_map, (T,), torch.int64), (carry, (N, HQ, K), torch.int64),
+                (carry_out, (N, HQ, K), torch.int64)):
+        _io_dtype(k_pages, k, v, g)
+        _expect("k", k, (T, H, K))
+        _expect("v", v, (T, H, V))
+        _expect("g", g, (T, HQ, K))
+        _expect("cu_q", cu_q, (N + 1,), torch.int32)
+        _expect("kv_lens", kv_lens, (N,), torch.int32)
+        _expect("slot_map", slot_map, (T,), torch.int64)
+        _expect("carry", carry, (N, HQ, K), torch.int64)
+        _expect("carry_out", carry_out, (N, HQ, K), torch.int64)
+        _same_device(k_pages, k, v, g, cu_q, kv_lens, slot_map, carry, carry_out)
+    p = k_pages.new_empty((T, HQ, K), dtype=torch.float32)
     nbytes = L.wall_paged_append_workspace(N, T, max_new, HQ, K, PS)
-    ws = _ws(nbytes, k_pages.device) if nbytes else None
+    ws = k_pages.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
     L.wall_paged_append(k.contiguous(), v.contiguous(), g.contiguous(), cu_q, kv_lens, slot_map,
                         N, T, max_new, H, HQ, K, V, PS, NP, k_pages, v_pages, r_pages, carry,
                         carry_out, p, ws)
@@ -636,22 +654,30 @@ def wall_paged_attn(q, p, cu_q, kv_lens, block_table, k_pages, v_pages, r_pages,
     if q.dim() != 3:
         raise ValueError("q must be [T, HQ, K]")
     T = q.shape[0]
-    _io_dtype(k_pages, q)
-    _expect("q", q, (T, HQ, K))
-    _expect("p", p, (T, HQ, K), torch.float32)
     N, max_new = _batch(cu_q, kv_lens, max_new, T)
     if block_table.dim() != 2 or block_table.shape[1] < 1:
         raise ValueError("block_table must be [N, max_pages]")
     MP = block_table.shape[1]
-    _expect("block_table", block_table, (N, MP), torch.int32)
-    sk = _opt_f32("sink_bias", sink_bias, (HQ,))
-    _same_device(k_pages, q, p, cu_q, kv_lens, block_table, sk)
-    dev = k_pages.device
-    o = torch.empty((T, HQ, V), dtype=q.dtype, device=dev)
-    lse = torch.empty((T, HQ), dtype=torch.float32, device=dev) if return_lse else None
-    ws = _ws(L.wall_paged_attn_workspace(q.dtype, N, T, max_new, H, HQ, K, V), dev)
+    sk = sink_bias
+    if not _are(k_pages.get_device(), (q, (T, HQ, K), k_pages.dtype),
+                (p, (T, HQ, K), torch.float32), (cu_q, (N + 1,), torch.int32),
+                (kv_lens, (N,), torch.int32), (block_table, (N, MP), torch.int32),
+                *(((sk, (HQ,), torch.float32),) if sk is not None else ())):
+        _io_dtype(k_pages, q)
+        _expect("q", q, (T, HQ, K))
+        _expect("p", p, (T, HQ, K), torch.float32)
+        _expect("cu_q", cu_q, (N + 1,), torch.int32)
+        _expect("kv_lens", kv_lens, (N,), torch.int32)
+        _expect("block_table", block_table, (N, MP), torch.int32)
+        sk = _opt_f32("sink_bias", sk, (HQ,))
+        _same_device(k_pages, q, p, cu_q, kv_lens, block_table, sk)
+    o = q.new_empty((T, HQ, V))
+    lse = q.new_empty((T, HQ), dtype=torch.float32) if return_lse else None
+    nbytes = L.wall_paged_attn_workspace(q.dtype, N, T, max_new, H, HQ, K, V)
+    ws = q.new_empty(max(nbytes, 1), dtype=torch.uint8)
     L.wall_paged_attn(q.contiguous(), p.contiguous(), cu_q, kv_lens, block_table, N, T, max_new,
-                      MP, H, HQ, K, V, PS, NP, k_pages, v_pages, r_pages, sk, scale or 0.0,
+                      MP, H, HQ, K, V, PS, NP, k_pages, v_pages, r_pages,
+                      sk.contiguous() if sk is not None else None, scale or 0.0,
                       window_size or 0, o, lse, ws)
     return (o, lse) if return_lse else o
 
