@@ -164,9 +164,9 @@ __device__ __forceinline__ Run run_of(const Cursor& c, long long left) {
 struct Share {
   long long W;
   int G;
-  __device__ __noinline__ long long begin(int c) const { return W * c / G; }
+  __device__ __forceinline__ long long begin(int c) const { return W * c / G; }
   // the CTA that holds place x
-  __device__ __noinline__ int owner(long long x) const {
+  __device__ __forceinline__ int owner(long long x) const {
     return (int)(((x + 1) * G + W - 1) / W) - 1;
   }
   // the CTA that holds the last tile of a unit whose place p is place x
@@ -198,7 +198,7 @@ __device__ __forceinline__ long long warp_incl_sum(long long x) {
 // and the places before that request.  No more CTAs share the work than leave
 // each `least` places.
 template <int TB, int U>
-__device__ __noinline__ bool find_start(const Batch& bt, int window, int heads, const Pick& pk,
+__device__ __forceinline__ bool find_start(const Batch& bt, int window, int heads, const Pick& pk,
                                            int least, int cta, int n_cta, FindScratch& fs,
                                            Share& sh) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
@@ -254,7 +254,7 @@ __device__ __noinline__ bool find_start(const Batch& bt, int window, int heads, 
 
 // The cursor at flattened place x, x inside request `req`, which begins at `base`.
 template <int TB, int U>
-__device__ __noinline__ Cursor cursor_at(const Batch& bt, int window, int req, long long base,
+__device__ __forceinline__ Cursor cursor_at(const Batch& bt, int window, int req, long long base,
                                             long long x) {
   Cursor c;
   c.r = request_of<TB>(bt, req, window);
@@ -276,7 +276,7 @@ __device__ __noinline__ Cursor cursor_at(const Batch& bt, int window, int req, l
 
 // To the next unit (there is one: the caller's places do not end here).
 template <int TB>
-__device__ __noinline__ void next_unit(const Batch& bt, int window, int heads, const Pick& pk,
+__device__ __forceinline__ void next_unit(const Batch& bt, int window, int heads, const Pick& pk,
                                           Cursor& c) {
   c.p = 0;
   if (++c.b == c.r.nb) {
@@ -294,10 +294,6 @@ __device__ __noinline__ void next_unit(const Batch& bt, int window, int heads, c
   }
   c.n_tiles = unit_tiles(c.r, c.b);
 }
-
-// (The functions above are calls, not inlined: they run once a unit or less, and
-// the tensor-core kernel's code has to stay within what the instruction cache
-// holds -- at 122 KB of it every role ran a third slower than at 78 KB.)
 
 // What the merge of a cut unit needs, written by the CTA that begins it.
 struct PartDesc {

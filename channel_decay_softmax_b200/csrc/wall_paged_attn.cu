@@ -18,25 +18,32 @@ using namespace paged;
 // general kernel: 32 query rows of one head against tiles of 32 keys, fp32
 // throughout.  Four warps of eight rows; lane = key for the scores (a key's
 // channels from shared memory, the rows' by broadcast: one load of keys feeds
-// eight rows), then lane = four value channels for P V.
+// eight rows), then lane = VPL value channels for P V (two up to V = 64, so
+// that no lane idles), P by broadcast from shared memory four keys at a time.
+// A row's reference is raised only when a score passes it by 2^8, and its sum
+// is kept by lanes until the end.
 
 constexpr int GR = kGeneralRows;
 constexpr int kGenWarps = 4, kGenThreads = kGenWarps * 32;
 constexpr int kRowsPerWarp = GR / kGenWarps;
 
-size_t gen_smem(int K, int V) { return sizeof(float) * (size_t)(GR * K + GR * (K + 4) + GR * V); }
+size_t gen_smem(int K, int V) {
+  return sizeof(float) * (size_t)(GR * K + GR * (K + 4) + GR * V + GR * GR);
+}
+
 
 // Tiles [ta, tb) of the row block: softmax state of this warp's rows.
-template <typename T>
+template <typename T, int VPL>
 __device__ __forceinline__ void gen_tiles(const AttnArgs& a, const Request& r, int h, int row0,
                                           int lo_tile, int ta, int tb, float* smem,
                                           float (&m)[kRowsPerWarp], float (&l)[kRowsPerWarp],
-                                          float (&acc)[kRowsPerWarp][4]) {
+                                          float (&acc)[kRowsPerWarp][VPL]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int K = a.K, V = a.V;
   float* sQ = smem;              // [GR][K]
   float* sK = sQ + GR * K;       // [GR][K + 4]
   float* sV = sK + GR * (K + 4); // [GR][V]
+  float* sP = sV + GR * V + (tid >> 5) * (kRowsPerWarp * GR);  // this warp's [rows][keys]
   const T* q = static_cast<const T*>(a.q);
   const T* kp = static_cast<const T*>(a.kp);
   const T* vp = static_cast<const T*>(a.vp);
@@ -50,9 +57,14 @@ __device__ __forceinline__ void gen_tiles(const AttnArgs& a, const Request& r, i
     m[x] = -INFINITY;
     l[x] = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[x][e] = 0.f;
+    for (int e = 0; e < VPL; ++e) acc[x][e] = 0.f;
   }
   if (r.dead) return;
+  // the rows' own pages: two at most, since a page has 32 positions or more
+  const int pos0 = r.ctx + row0;
+  const int own0 = pos0 >> a.shift, own1 = (pos0 + ni - 1) >> a.shift;
+  const int page0 = own0 < a.MP ? page_of(a.table, trow, own0, a.NP) : -1;
+  const int page1 = own1 < a.MP ? page_of(a.table, trow, own1, a.NP) : -1;
   int at = -1;  // table slot whose scaled queries are in sQ
   for (int t = ta; t < tb; ++t) {
     const int j0 = (lo_tile + t) * GR;
@@ -63,40 +75,52 @@ __device__ __forceinline__ void gen_tiles(const AttnArgs& a, const Request& r, i
       continue;
     }
     __syncthreads();  // the last tile's readers are done
-    if (slot != at) {
-      const int* Rc = a.rp + ((long)page * a.HQ + h) * K;
-      for (int idx = tid; idx < GR * K; idx += kGenThreads) {
-        const int row = idx / K, c = idx - row * K;
-        float x = 0.f;
-        if (row < ni) {
-          const int rs = (r.ctx + row0 + row) >> a.shift;
-          if (rs >= slot) {  // rows of an earlier page see nothing of this one
-            const int rpage = rs < a.MP ? page_of(a.table, trow, rs, a.NP) : -1;
-            const int Rr = rpage >= 0 ? a.rp[((long)rpage * a.HQ + h) * K + c] : 0;
-            const long e = ((long)(r.t0 + row0 + row) * a.HQ + h) * K + c;
-            x = a.scale_log2 * to_f32(q[e]) * exp2f(a.p[e] + (float)(Rr - Rc[c]));
-          }
-        }
-        sQ[idx] = x;
-      }
-      at = slot;
-    }
     const int off = j0 & ((1 << a.shift) - 1);
     const T* kt = kp + ((((long)page * a.HQ + h) << a.shift) + off) * K;
     const T* vt = vp + ((((long)page * a.H + kh) << a.shift) + off) * V;
+    const int nk = r.kv - j0;  // keys of the tile; what lies behind them is not read
+#pragma unroll 4
     for (int idx = tid; idx < GR * (K / 8); idx += kGenThreads) {
       const int j = idx / (K / 8), c = (idx - j * (K / 8)) * 8;
       float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (j0 + j < r.kv) load8(kt + (long)j * K + c, x);
+      if (j < nk) load8(kt + j * K + c, x);
       *reinterpret_cast<float4*>(sK + j * (K + 4) + c) = make_float4(x[0], x[1], x[2], x[3]);
       *reinterpret_cast<float4*>(sK + j * (K + 4) + c + 4) = make_float4(x[4], x[5], x[6], x[7]);
     }
+#pragma unroll 4
     for (int idx = tid; idx < GR * (V / 8); idx += kGenThreads) {
       const int j = idx / (V / 8), c = (idx - j * (V / 8)) * 8;
       float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (j0 + j < r.kv) load8(vt + (long)j * V + c, x);
+      if (j < nk) load8(vt + j * V + c, x);
       *reinterpret_cast<float4*>(sV + j * V + c) = make_float4(x[0], x[1], x[2], x[3]);
       *reinterpret_cast<float4*>(sV + j * V + c + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    }
+    if (slot != at) {
+      // the rows against this page: scale * log2(e) * q * 2^(p + R - R_c); rows
+      // of an earlier page see nothing of it
+      const int* Rc = a.rp + ((long)page * a.HQ + h) * K;
+      const int* R0 = a.rp + ((long)max(page0, 0) * a.HQ + h) * K;
+      const int* R1 = a.rp + ((long)max(page1, 0) * a.HQ + h) * K;
+      const long e0 = ((long)(r.t0 + row0) * a.HQ + h) * K;
+#pragma unroll 2
+      for (int idx = tid; idx < ni * (K / 8); idx += kGenThreads) {
+        const int row = idx / (K / 8), c = (idx - row * (K / 8)) * 8;
+        const int rs = (pos0 + row) >> a.shift;
+        const int* Rr = rs == own0 ? R0 : R1;
+        float qv[8], pv[8];
+        load8(q + e0 + (long)row * a.HQ * K + c, qv);
+        load8(a.p + e0 + (long)row * a.HQ * K + c, pv);
+        const int4 u0 = *reinterpret_cast<const int4*>(Rr + c), u1 = *reinterpret_cast<const int4*>(Rr + c + 4);
+        const int4 w0 = *reinterpret_cast<const int4*>(Rc + c), w1 = *reinterpret_cast<const int4*>(Rc + c + 4);
+        const int d[8] = {u0.x - w0.x, u0.y - w0.y, u0.z - w0.z, u0.w - w0.w,
+                          u1.x - w1.x, u1.y - w1.y, u1.z - w1.z, u1.w - w1.w};
+        const bool sees = rs >= slot;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          qv[e] = sees ? a.scale_log2 * qv[e] * exp2f(pv[e] + (float)d[e]) : 0.f;
+        store8(sQ + row * K + c, qv);
+      }
+      at = slot;
     }
     __syncthreads();
     if (w0 >= ni) continue;  // warps past the block's rows only keep step
@@ -104,6 +128,7 @@ __device__ __forceinline__ void gen_tiles(const AttnArgs& a, const Request& r, i
 #pragma unroll
     for (int x = 0; x < kRowsPerWarp; ++x) d[x] = 0.f;
     const float* krow = sK + lane * (K + 4);
+#pragma unroll 4
     for (int c = 0; c < K; c += 4) {
       const float4 kx = *reinterpret_cast<const float4*>(krow + c);
 #pragma unroll
@@ -113,52 +138,71 @@ __device__ __forceinline__ void gen_tiles(const AttnArgs& a, const Request& r, i
       }
     }
     const int j = j0 + lane;
-    unsigned seen[kRowsPerWarp];
-    float pr[kRowsPerWarp];
+    unsigned seen[kRowsPerWarp], every = 0xffffffffu;
+    __syncwarp();  // the last tile's P has been read
 #pragma unroll
     for (int x = 0; x < kRowsPerWarp; ++x) {
       const int pos = r.ctx + row0 + w0 + x;
       const bool vis = w0 + x < ni && j <= pos && j < r.kv && pos - j < win;
       seen[x] = __ballot_sync(0xffffffffu, vis);
-      const float s = vis ? d[x] : -INFINITY;
-      float mx = s;
+      if (w0 + x < ni) every &= seen[x];
+      // (m = -inf: the row's first key)
+      if (__any_sync(0xffffffffu, vis && d[x] > m[x] + 8.f)) {
+        float mx = vis ? d[x] : -INFINITY;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float mn = fmaxf(m[x], mx);
-      const float use = mn == -INFINITY ? 0.f : mn;
-      const float alpha = exp2f(m[x] - use);
-      pr[x] = vis ? exp2f(s - use) : 0.f;
-      float ps = pr[x];
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mx = fmaxf(mx, m[x]);
+        const float alpha = exp2f(m[x] - mx);
+        l[x] *= alpha;
+        m[x] = mx;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
-      l[x] = l[x] * alpha + ps;
-      m[x] = mn;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[x][e] *= alpha;
+        for (int e = 0; e < VPL; ++e) acc[x][e] *= alpha;
+      }
+      const float p = vis ? exp2f(d[x] - (m[x] == -INFINITY ? 0.f : m[x])) : 0.f;
+      l[x] += p;
+      sP[x * GR + lane] = p;
     }
-    // a masked key's value row may hold anything (NaN included): it is
-    // skipped, not multiplied by zero
-    for (int jj = 0; jj < GR; ++jj) {
-      float4 vx = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (lane * 4 < V) vx = *reinterpret_cast<const float4*>(sV + jj * V + lane * 4);
+    __syncwarp();
+    const float* vcol = sV + (lane * VPL < V ? lane * VPL : 0);
+#pragma unroll 1
+    for (int jj = 0; jj < GR; jj += 4) {
+      float v[4][VPL];
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        if constexpr (VPL == 4) {
+          const float4 u = *reinterpret_cast<const float4*>(vcol + (jj + z) * V);
+          v[z][0] = u.x; v[z][1] = u.y; v[z][2] = u.z; v[z][3] = u.w;
+        } else {
+          const float2 u = *reinterpret_cast<const float2*>(vcol + (jj + z) * V);
+          v[z][0] = u.x; v[z][1] = u.y;
+        }
+      }
 #pragma unroll
       for (int x = 0; x < kRowsPerWarp; ++x) {
-        const float pj = __shfl_sync(0xffffffffu, pr[x], jj);
-        if ((seen[x] >> jj) & 1u) {
-          acc[x][0] = fmaf(pj, vx.x, acc[x][0]);
-          acc[x][1] = fmaf(pj, vx.y, acc[x][1]);
-          acc[x][2] = fmaf(pj, vx.z, acc[x][2]);
-          acc[x][3] = fmaf(pj, vx.w, acc[x][3]);
-        }
+        const float4 p4 = *reinterpret_cast<const float4*>(sP + x * GR + jj);
+        const float p[4] = {p4.x, p4.y, p4.z, p4.w};
+        // a masked key's value row may hold anything (NaN included): it is
+        // skipped, not multiplied by zero
+        const unsigned bits = every == 0xffffffffu ? 15u : seen[x] >> jj;
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          if ((bits >> z) & 1u) {
+#pragma unroll
+            for (int e = 0; e < VPL; ++e) acc[x][e] = fmaf(p[z], v[z][e], acc[x][e]);
+          }
       }
     }
   }
+#pragma unroll
+  for (int x = 0; x < kRowsPerWarp; ++x)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l[x] += __shfl_xor_sync(0xffffffffu, l[x], o);
 }
 
 // The finished rows of a block: o = acc / l and lse, the sink's weight in l.
-template <typename T>
+template <typename T, int VPL>
 __device__ __forceinline__ void write_row(const AttnArgs& a, long token, int h, int lane, float m,
-                                          float l, const float (&acc)[4]) {
+                                          float l, const float (&acc)[VPL]) {
   float mf = m, lt = l, f = 1.f;
   if (a.sink) {
     const float sk = a.sink[h] * kLog2e;
@@ -167,16 +211,16 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, long token, int h, 
     lt = l * f + exp2f(sk - mf);
   }
   const float inv = lt > 0.f || lt != lt ? f / lt : 0.f;  // a row that sees nothing: 0
-  if (lane * 4 < a.V) {
-    T* o = static_cast<T*>(a.o) + ((long)token * a.HQ + h) * a.V + lane * 4;
+  if (lane * VPL < a.V) {
+    T* o = static_cast<T*>(a.o) + ((long)token * a.HQ + h) * a.V + lane * VPL;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = from_f32<T>(acc[e] * inv);
+    for (int e = 0; e < VPL; ++e) o[e] = from_f32<T>(acc[e] * inv);
   }
   if (lane == 0 && a.lse) a.lse[token * a.HQ + h] = lt == 0.f ? -INFINITY : (mf + log2f(lt)) * kLn2;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kGenThreads) general_kernel(AttnArgs a, Pick pk, Parts parts) {
+template <typename T, int VPL>
+__global__ void __launch_bounds__(kGenThreads, 3) general_kernel(AttnArgs a, Pick pk, Parts parts) {
   extern __shared__ __align__(16) float gen_shared[];
   __shared__ FindScratch fs;
   const int cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -188,8 +232,8 @@ __global__ void __launch_bounds__(kGenThreads) general_kernel(AttnArgs a, Pick p
   for (long long x = x0; x < x1;) {
     const Run run = run_of<0>(c, x1 - x);
     const int ta = run.ta, tb = run.tb;
-    float m[kRowsPerWarp], l[kRowsPerWarp], acc[kRowsPerWarp][4];
-    gen_tiles<T>(a, c.r, c.h, c.b * GR, tile_lo(c.r, c.b), ta, tb, gen_shared, m, l, acc);
+    float m[kRowsPerWarp], l[kRowsPerWarp], acc[kRowsPerWarp][VPL];
+    gen_tiles<T, VPL>(a, c.r, c.h, c.b * GR, tile_lo(c.r, c.b), ta, tb, gen_shared, m, l, acc);
     const int ni = min(GR, c.r.n - c.b * GR);
     const bool whole = ta == 0 && tb == c.n_tiles;
     const int slot = ta == 0 ? 1 : 0;
@@ -200,11 +244,14 @@ __global__ void __launch_bounds__(kGenThreads) general_kernel(AttnArgs a, Pick p
       const int row = warp * kRowsPerWarp + y;
       if (row >= ni) continue;
       if (whole) {
-        write_row<T>(a, c.r.t0 + c.b * GR + row, c.h, lane, m[y], l[y], acc[y]);
+        write_row<T, VPL>(a, c.r.t0 + c.b * GR + row, c.h, lane, m[y], l[y], acc[y]);
       } else {
-        if (lane * 4 < a.V)
-          *reinterpret_cast<float4*>(po + (size_t)row * a.V + lane * 4) =
-              make_float4(acc[y][0], acc[y][1], acc[y][2], acc[y][3]);
+        if (lane * VPL < a.V) {
+#pragma unroll
+          for (int e = 0; e < VPL; e += 2)
+            *reinterpret_cast<float2*>(po + (size_t)row * a.V + lane * VPL + e) =
+                make_float2(acc[y][e], acc[y][e + 1]);
+        }
         if (lane == 0) {
           pm[row * 2] = m[y];
           pm[row * 2 + 1] = l[y];
@@ -225,8 +272,8 @@ __global__ void __launch_bounds__(kGenThreads) general_kernel(AttnArgs a, Pick p
 // The units that the tensor-core kernel flagged, again and whole: a grid over
 // (request's 128-row block, head, 32 rows of it), whose CTAs read one word and
 // leave when nothing is flagged.
-template <typename T>
-__global__ void __launch_bounds__(kGenThreads) flagged_kernel(AttnArgs a, UnitFlags flags) {
+template <typename T, int VPL>
+__global__ void __launch_bounds__(kGenThreads, 3) flagged_kernel(AttnArgs a, UnitFlags flags) {
   extern __shared__ __align__(16) float gen_shared[];
   if (*flags.any(a.HQ) == 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -240,12 +287,12 @@ __global__ void __launch_bounds__(kGenThreads) flagged_kernel(AttnArgs a, UnitFl
     for (int x = first; x < items; x += gridDim.x) {
       const int b = x / a.HQ, h = x - b * a.HQ;
       if (flags.f[flags.place(r, b * GR / kChunkRows) * a.HQ + h] == 0) continue;
-      float m[kRowsPerWarp], l[kRowsPerWarp], acc[kRowsPerWarp][4];
-      gen_tiles<T>(a, r, h, b * GR, tile_lo(r, b), 0, unit_tiles(r, b), gen_shared, m, l, acc);
+      float m[kRowsPerWarp], l[kRowsPerWarp], acc[kRowsPerWarp][VPL];
+      gen_tiles<T, VPL>(a, r, h, b * GR, tile_lo(r, b), 0, unit_tiles(r, b), gen_shared, m, l, acc);
 #pragma unroll
       for (int y = 0; y < kRowsPerWarp; ++y) {
         const int row = b * GR + warp * kRowsPerWarp + y;
-        if (row < n) write_row<T>(a, r.t0 + row, h, lane, m[y], l[y], acc[y]);
+        if (row < n) write_row<T, VPL>(a, r.t0 + row, h, lane, m[y], l[y], acc[y]);
       }
     }
     at = (at + items) % (int)gridDim.x;
@@ -312,8 +359,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, Parts pa
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (group > 0) write_row<T>(a, t0, d.h * group + row, lane, m, l, acc);
-    else write_row<T>(a, t0 + (long)d.b * parts.rows + row, d.h, lane, m, l, acc);
+    if (group > 0) write_row<T, 4>(a, t0, d.h * group + row, lane, m, l, acc);
+    else write_row<T, 4>(a, t0 + (long)d.b * parts.rows + row, d.h, lane, m, l, acc);
   }
 }
 
@@ -325,23 +372,32 @@ int join(const AttnArgs& a, const Parts& parts, int group, cudaStream_t stream) 
   return cudaGetLastError() == cudaSuccess ? WALL_OK : WALL_ERR_CUDA;
 }
 
+template <typename T, int VPL>
+int launch_general(const AttnArgs& a, const Pick& pk, const Parts& parts, cudaStream_t stream) {
+  static bool attr[kMaxDevices] = {};
+  if (!set_max_smem_once(general_kernel<T, VPL>, (int)gen_smem(128, 128), attr)) return WALL_ERR_CUDA;
+  general_kernel<T, VPL><<<parts.n_cta, kGenThreads, gen_smem(a.K, a.V), stream>>>(a, pk, parts);
+  return cudaGetLastError() == cudaSuccess ? WALL_OK : WALL_ERR_CUDA;
+}
 template <typename T>
 int run_general(const AttnArgs& a, const Pick& pk, const Parts& parts, cudaStream_t stream) {
-  static bool attr[kMaxDevices] = {};
-  if (!set_max_smem_once(general_kernel<T>, (int)gen_smem(128, 128), attr)) return WALL_ERR_CUDA;
-  general_kernel<T><<<parts.n_cta, kGenThreads, gen_smem(a.K, a.V), stream>>>(a, pk, parts);
-  if (cudaGetLastError() != cudaSuccess) return WALL_ERR_CUDA;
-  return join<T>(a, parts, 0, stream);
+  const int rc = a.V <= 64 ? launch_general<T, 2>(a, pk, parts, stream)
+                           : launch_general<T, 4>(a, pk, parts, stream);
+  return rc ? rc : join<T>(a, parts, 0, stream);
 }
 
 size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
-template <typename T>
-int run_flagged(const AttnArgs& a, const UnitFlags& flags, cudaStream_t stream) {
+template <int VPL>
+int launch_flagged(const AttnArgs& a, const UnitFlags& flags, cudaStream_t stream) {
+  using T = __nv_bfloat16;
   static bool attr[kMaxDevices] = {};
-  if (!set_max_smem_once(flagged_kernel<T>, (int)gen_smem(128, 128), attr)) return WALL_ERR_CUDA;
-  flagged_kernel<T><<<kGeneralCtas, kGenThreads, gen_smem(a.K, a.V), stream>>>(a, flags);
+  if (!set_max_smem_once(flagged_kernel<T, VPL>, (int)gen_smem(128, 128), attr)) return WALL_ERR_CUDA;
+  flagged_kernel<T, VPL><<<kGeneralCtas, kGenThreads, gen_smem(a.K, a.V), stream>>>(a, flags);
   return cudaGetLastError() == cudaSuccess ? WALL_OK : WALL_ERR_CUDA;
+}
+int run_flagged(const AttnArgs& a, const UnitFlags& flags, cudaStream_t stream) {
+  return a.V <= 64 ? launch_flagged<2>(a, flags, stream) : launch_flagged<4>(a, flags, stream);
 }
 
 // Which kernels a call runs: single-token rows stream through the decode
@@ -433,7 +489,7 @@ int paged_attn(const PagedAttnProblem& pb, void* ws, cudaStream_t stream) {
     if (rc) return rc;
     rc = join<__nv_bfloat16>(a, p, 0, stream);
     if (rc) return rc;
-    rc = run_flagged<__nv_bfloat16>(a, flags, stream);
+    rc = run_flagged(a, flags, stream);
     if (rc) return rc;
   }
   if (r.general) {

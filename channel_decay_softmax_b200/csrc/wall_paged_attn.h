@@ -8,9 +8,9 @@ namespace wall {
 namespace paged {
 
 // CTAs that share the tiles of a batch, for each kind of kernel: one per SM
-// for the kernels that fill an SM's shared memory, four for the general one.
+// for the kernels that fill an SM's shared memory, three for the general one.
 constexpr int kSms = 148;
-constexpr int kGeneralCtas = kSms * 4;
+constexpr int kGeneralCtas = kSms * 3;
 constexpr int kGeneralRows = 32;  // query rows of a general unit, keys of a tile
 constexpr int kChunkRows = 128;   // the same of the tensor-core kernel
 

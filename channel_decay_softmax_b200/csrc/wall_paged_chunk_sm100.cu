@@ -55,6 +55,28 @@ constexpr float kRaiseAbove = 256.f;      // a tile's sum of P that raises the r
 constexpr float kFlagAbove = 1.2676506e30f;  // 2^100: one that may not be held
 constexpr int kUnit = 3;                  // a unit's own cost, in tiles
 
+// The walk over the units as calls: it runs once a unit or less, and the code of
+// this kernel's roles has to stay within what the instruction cache holds (at
+// 122 KB of it every role ran a third slower than at 83 KB).
+__device__ __noinline__ bool start_share(const Batch& bt, int window, int heads, int cta, int n_cta,
+                                         FindScratch& fs, Share& sh, long long& x0, long long& x1) {
+  if (!find_start<BM, kUnit>(bt, window, heads, {2, 0x7fffffff}, kUnit + 2, cta, n_cta, fs, sh))
+    return false;
+  x0 = sh.begin(cta);
+  x1 = sh.begin(cta + 1);
+  return true;
+}
+__device__ __noinline__ void start_cursor(const Batch& bt, int window, const FindScratch& fs,
+                                          long long x, Cursor& c) {
+  c = cursor_at<BM, kUnit>(bt, window, fs.req, fs.base, x);
+}
+__device__ __noinline__ void advance(const Batch& bt, int window, int heads, Cursor& c) {
+  next_unit<BM>(bt, window, heads, {2, 0x7fffffff}, c);
+}
+__device__ __noinline__ int ending_cta(const Share& sh, const Cursor& c, long long x) {
+  return sh.last_owner<kUnit>(c, x);
+}
+
 // A CTA's piece of one unit, as every role reads it.
 struct Segment {
   int t0, ni;       // first query row among the packed ones, rows
@@ -261,9 +283,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
   }
   Share sh;
-  if (!find_start<BM, kUnit>(a.bt, a.window, a.HQ, {2, 0x7fffffff}, kUnit + 2, cta, parts.n_cta, fs,
-                             sh))
-    return;
+  long long x0, x1;
+  if (!start_share(a.bt, a.window, a.HQ, cta, parts.n_cta, fs, sh, x0, x1)) return;
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_holder), 512);
     tmem_relinquish();
@@ -294,9 +315,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto table_at = [&](int req, int slot) {
       return slot + lane < a.MP ? page_of(a.table, (long)req * a.MP, slot + lane, a.NP) : -1;
     };
-    long long x = sh.begin(cta);
-    const long long x1 = sh.begin(cta + 1);
-    Cursor c = cursor_at<BM, kUnit>(a.bt, a.window, fs.req, fs.base, x);
+    long long x = x0;
+    Cursor c;
+    start_cursor(a.bt, a.window, fs, x, c);
     int slot_k = 0, ids_k = 0, seg_k = -1;
     // the figures of the next unit that this CTA has tiles of, into the ring;
     // returns their number, 0 at the share's end
@@ -329,12 +350,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0 && run.ta == 0 && !s.whole) {
             PartDesc d;
             d.req = s.req; d.h = s.h; d.b = c.b;
-            d.last_cta = sh.last_owner<kUnit>(c, x);
+            d.last_cta = ending_cta(sh, c, x);
             parts.desc[cta] = d;
           }
         }
         x += run.places;
-        if (x < x1) next_unit<BM>(a.bt, a.window, a.HQ, {2, 0x7fffffff}, c);
+        if (x < x1) advance(a.bt, a.window, a.HQ, c);
         if (s.cnt > 0) break;
       }
       ++seg_k;
