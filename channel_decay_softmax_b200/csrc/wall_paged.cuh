@@ -297,7 +297,7 @@ __device__ __forceinline__ void next_unit(const Batch& bt, int window, int heads
 
 // What the merge of a cut unit needs, written by the CTA that begins it.
 struct PartDesc {
-  int req, h, b;
+  int t0, rows, h;  // its first token, its rows (of one kv head: unused)
   int last_cta;  // < 0: this CTA begins no unit that another one ends
 };
 

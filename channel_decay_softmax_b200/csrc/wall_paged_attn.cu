@@ -7,6 +7,8 @@
 // where k_jn is the cached row (k 2^(R - P)), p the token's prefix beyond its
 // page's anchor and R the pages' whole-number anchors: the query meets each
 // page once, scaled, and the inner loop has no gate arithmetic.
+#include <algorithm>
+
 #include "wall_paged_attn.h"
 
 namespace wall {
@@ -213,8 +215,10 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, long token, int h, 
   const float inv = lt > 0.f || lt != lt ? f / lt : 0.f;  // a row that sees nothing: 0
   if (lane * VPL < a.V) {
     T* o = static_cast<T*>(a.o) + ((long)token * a.HQ + h) * a.V + lane * VPL;
+    struct alignas(sizeof(T) * VPL) Out { T x[VPL]; } out;  // one store a lane
 #pragma unroll
-    for (int e = 0; e < VPL; ++e) o[e] = from_f32<T>(acc[e] * inv);
+    for (int e = 0; e < VPL; ++e) out.x[e] = from_f32<T>(acc[e] * inv);
+    *reinterpret_cast<Out*>(o) = out;
   }
   if (lane == 0 && a.lse) a.lse[token * a.HQ + h] = lt == 0.f ? -INFINITY : (mf + log2f(lt)) * kLn2;
 }
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(kGenThreads, 3) general_kernel(AttnArgs a, Pic
     }
     if (!whole && slot == 1 && threadIdx.x == 0) {
       PartDesc d;
-      d.req = c.r.i; d.h = c.h; d.b = c.b;
+      d.t0 = c.r.t0 + c.b * GR; d.rows = min(GR, c.r.n - c.b * GR); d.h = c.h;
       d.last_cta = sh.last_owner<0>(c, x);
       parts.desc[cta] = d;
     }
@@ -303,72 +307,99 @@ __global__ void __launch_bounds__(kGenThreads, 3) flagged_kernel(AttnArgs a, Uni
 // Joining the units that more than one CTA worked on: o = sum of the parts
 // weighted by 2^(m_part - m), over the sum of their l, in the order of the
 // CTAs (the same bits every time).  One warp a row; 4 channels a lane.
-// group > 0: a part's rows are the heads of one kv head, of a single token.
-constexpr int kJoinThreads = 256;
+// One launch joins all of a call's parts, of the two kernels that it may run.
+constexpr int kJoinThreads = 256, kJoinY = 4;
+struct JoinSet {
+  Parts parts;
+  int group;  // > 0: a part's rows are the heads of one kv head, of a single token
+};
+struct JoinSets {
+  JoinSet s[2];
+  int n;
+};
 template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, Parts parts, int group) {
+__global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(AttnArgs a, JoinSets sets) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int cta = blockIdx.x;
-  if (cta == 0 && blockIdx.y == 0)
+  const bool second = (int)blockIdx.x >= sets.s[0].parts.n_cta;
+  const Parts parts = second ? sets.s[1].parts : sets.s[0].parts;
+  const int group = second ? sets.s[1].group : sets.s[0].group;
+  const int cta = blockIdx.x - (second ? sets.s[0].parts.n_cta : 0);
+  if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int i = threadIdx.x; i < a.bt.N; i += kJoinThreads)
       if (a.bt.rows(i) > a.max_new) record_status(a.status, WALL_ERR_INVALID_ARG);
   const PartDesc d = parts.desc[cta];
   if (d.last_cta < 0) return;
-  const int t0 = a.bt.start(d.req), n = a.bt.rows(d.req);
-  const int rows = group > 0 ? group : min(parts.rows, n - d.b * parts.rows);
   const int np = d.last_cta - cta + 1;
   const int stride = gridDim.y * (kJoinThreads / 32);
-  for (int row = blockIdx.y * (kJoinThreads / 32) + warp; row < rows; row += stride) {
+  const size_t step = parts.stride(a.V) * 2;  // from a CTA's part to the next CTA's
+#pragma unroll 1
+  for (int row = blockIdx.y * (kJoinThreads / 32) + warp; row < d.rows; row += stride) {
+    // part s > 0 is at s * step from CTA `cta`'s slot 0; part 0 is its slot 1
+    const float2* ml = reinterpret_cast<const float2*>(parts.ml(cta, 0, a.V)) + row;
+    const float* o = parts.o(cta, 0, a.V) + row * a.V + (lane * 4 < a.V ? lane * 4 : 0);
     float m = -INFINITY;
-    for (int s = lane; s < np; s += 32)
-      m = fmaxf(m, parts.ml(cta + s, s == 0 ? 1 : 0, a.V)[row * 2]);
+#pragma unroll 1
+    for (int s = lane; s < np; s += 32) m = fmaxf(m, ml[(s == 0 ? step : s * step * 2) / 4].x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
     float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
     for (int s0 = 0; s0 < np; s0 += 32) {
       float f = 0.f;
-      if (s0 + lane < np) {
-        const float* ml = parts.ml(cta + s0 + lane, s0 + lane == 0 ? 1 : 0, a.V) + row * 2;
-        if (ml[0] != -INFINITY) {
-          f = exp2f(ml[0] - m);
-          l = fmaf(ml[1], f, l);
+      const int s = s0 + lane;
+      if (s < np) {
+        const float2 y = ml[(s == 0 ? step : s * step * 2) / 4];
+        if (y.x != -INFINITY) {
+          f = exp2f(y.x - m);
+          l = fmaf(y.y, f, l);
         }
       }
       const int cnt = min(32, np - s0);
-      for (int j0 = 0; j0 < cnt; j0 += 8) {
-        float4 x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int s = s0 + min(j0 + j, cnt - 1);
-          x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (lane * 4 < a.V)
-            x[j] = *reinterpret_cast<const float4*>(parts.o(cta + s, s == 0 ? 1 : 0, a.V) +
-                                                    (size_t)row * a.V + lane * 4);
+      const float* os = o + s0 * step;
+      auto add = [&](float4 x, int j) {
+        const float fj = __shfl_sync(0xffffffffu, f, j);
+        if (fj != 0.f) {
+          acc[0] = fmaf(x.x, fj, acc[0]);
+          acc[1] = fmaf(x.y, fj, acc[1]);
+          acc[2] = fmaf(x.z, fj, acc[2]);
+          acc[3] = fmaf(x.w, fj, acc[3]);
         }
+      };
+      auto part = [&](int j) {
+        return *reinterpret_cast<const float4*>(os + (s0 + j == 0 ? step / 2 : j * step));
+      };
+      int j = 0;
+#pragma unroll 1
+      for (; j + 4 <= cnt; j += 4) {
+        float4 x[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float fj = __shfl_sync(0xffffffffu, f, (j0 + j) & 31);
-          if (j0 + j < cnt && fj != 0.f) {
-            acc[0] = fmaf(x[j].x, fj, acc[0]);
-            acc[1] = fmaf(x[j].y, fj, acc[1]);
-            acc[2] = fmaf(x[j].z, fj, acc[2]);
-            acc[3] = fmaf(x[j].w, fj, acc[3]);
-          }
-        }
+        for (int y = 0; y < 4; ++y) x[y] = part(j + y);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) add(x[y], j + y);
+      }
+#pragma unroll 1
+      for (; j < cnt; j += 2) {  // most units have two parts
+        const float4 x0 = part(j), x1 = part(min(j + 1, cnt - 1));
+        add(x0, j);
+        if (j + 1 < cnt) add(x1, j + 1);
       }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (group > 0) write_row<T, 4>(a, t0, d.h * group + row, lane, m, l, acc);
-    else write_row<T, 4>(a, t0 + (long)d.b * parts.rows + row, d.h, lane, m, l, acc);
+    for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    if (group > 0) write_row<T, 4>(a, d.t0, d.h * group + row, lane, m, l, acc);
+    else write_row<T, 4>(a, d.t0 + row, d.h, lane, m, l, acc);
   }
 }
 
 template <typename T>
-int join(const AttnArgs& a, const Parts& parts, int group, cudaStream_t stream) {
-  const int rows = group > 0 ? group : parts.rows;
-  join_kernel<T><<<dim3(parts.n_cta, ceil_div(rows, kJoinThreads / 32)), kJoinThreads, 0, stream>>>(
-      a, parts, group);
+int join(const AttnArgs& a, const JoinSets& sets, cudaStream_t stream) {
+  int ctas = 0, rows = 0;
+  for (int i = 0; i < sets.n; ++i) {
+    const JoinSet& s = sets.s[i];
+    ctas += s.parts.n_cta;
+    rows = std::max(rows, s.group > 0 ? s.group : s.parts.rows);
+  }
+  join_kernel<T><<<dim3(ctas, std::min(kJoinY, ceil_div(rows, kJoinThreads / 32))), kJoinThreads, 0, stream>>>(a, sets);
   return cudaGetLastError() == cudaSuccess ? WALL_OK : WALL_ERR_CUDA;
 }
 
@@ -381,9 +412,8 @@ int launch_general(const AttnArgs& a, const Pick& pk, const Parts& parts, cudaSt
 }
 template <typename T>
 int run_general(const AttnArgs& a, const Pick& pk, const Parts& parts, cudaStream_t stream) {
-  const int rc = a.V <= 64 ? launch_general<T, 2>(a, pk, parts, stream)
-                           : launch_general<T, 4>(a, pk, parts, stream);
-  return rc ? rc : join<T>(a, parts, 0, stream);
+  return a.V <= 64 ? launch_general<T, 2>(a, pk, parts, stream)
+                   : launch_general<T, 4>(a, pk, parts, stream);
 }
 
 size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -472,32 +502,39 @@ int paged_attn(const PagedAttnProblem& pb, void* ws, cudaStream_t stream) {
   a.status = device_status();
   const Route r = route_of(pb.dtype, pb.max_new, pb.H, pb.HQ, pb.K, pb.V);
   const AttnWs w = attn_ws(r, pb.N, pb.T, pb.H, pb.HQ, pb.K, pb.V);
+  UnitFlags flags = {};
+  if (r.chunk) {
+    flags.f = reinterpret_cast<int*>(static_cast<char*>(ws) + w.flags);
+    flags.places_n = (int)UnitFlags::places(pb.N, pb.T);
+    flags.total = UnitFlags::count(pb.N, pb.T, pb.HQ);
+  }
+  JoinSets sets = {};
   if (r.decode) {
     const int G = pb.HQ / pb.H;
     const Parts p = parts_at(ws, w.dec_desc, w.dec_data, G, kSms);
-    int rc = decode_rows(a, p, stream);
+    const int rc = decode_rows(a, p, flags, stream);  // clears the flags
     if (rc) return rc;
-    rc = join<__nv_bfloat16>(a, p, G, stream);
-    if (rc) return rc;
+    sets.s[sets.n++] = {p, G};
+  } else if (r.chunk && cudaMemsetAsync(flags.f, 0, sizeof(int) * flags.total, stream) != cudaSuccess) {
+    return WALL_ERR_CUDA;
   }
   if (r.chunk) {
     const Parts p = parts_at(ws, w.chunk_desc, w.chunk_data, kChunkRows, kSms);
-    UnitFlags flags;
-    flags.f = reinterpret_cast<int*>(static_cast<char*>(ws) + w.flags);
-    flags.places_n = (int)UnitFlags::places(pb.N, pb.T);
-    int rc = chunk_rows(a, p, flags, static_cast<char*>(ws) + w.qh, stream);
+    const int rc = chunk_rows(a, p, flags, static_cast<char*>(ws) + w.qh, stream);
     if (rc) return rc;
-    rc = join<__nv_bfloat16>(a, p, 0, stream);
-    if (rc) return rc;
-    rc = run_flagged(a, flags, stream);
-    if (rc) return rc;
+    sets.s[sets.n++] = {p, 0};
   }
   if (r.general) {
     const Parts p = parts_at(ws, w.gen_desc, w.gen_data, GR, kGeneralCtas);
-    return pb.dtype == WALL_BF16 ? run_general<__nv_bfloat16>(a, r.rows, p, stream)
-                                 : run_general<float>(a, r.rows, p, stream);
+    const int rc = pb.dtype == WALL_BF16 ? run_general<__nv_bfloat16>(a, r.rows, p, stream)
+                                         : run_general<float>(a, r.rows, p, stream);
+    if (rc) return rc;
+    sets.s[sets.n++] = {p, 0};
   }
-  return WALL_OK;
+  const int rc = pb.dtype == WALL_BF16 ? join<__nv_bfloat16>(a, sets, stream)
+                                       : join<float>(a, sets, stream);
+  if (rc) return rc;
+  return r.chunk ? run_flagged(a, flags, stream) : WALL_OK;
 }
 
 }  // namespace wall

@@ -63,6 +63,7 @@ struct UnitFlags {
   __host__ __device__ static long places(int N, int T) { return (long)T / kChunkRows + N; }
   __host__ __device__ static long count(int N, int T, int HQ) { return places(N, T) * HQ + 1; }
   int places_n;
+  long total;  // count(N, T, HQ); 0: the call has none
   __device__ __forceinline__ int* any(int HQ) const { return f + (long)places_n * HQ; }
   __device__ __forceinline__ long place(const Request& r, int b) const {
     return (long)r.t0 / kChunkRows + r.i + b;
@@ -80,9 +81,10 @@ bool chunk_rows_supported(int dtype, int K, int V);
 int chunk_rows(const AttnArgs& a, const Parts& parts, const UnitFlags& flags, void* qh,
                cudaStream_t stream);
 
-// single-token rows (wall_paged_decode.cu): Parts of HQ / H rows, kSms CTAs
+// single-token rows (wall_paged_decode.cu): Parts of HQ / H rows, kSms CTAs; it
+// also clears the flags of the call's other units
 bool decode_rows_supported(int dtype, int H, int HQ, int K, int V);
-int decode_rows(const AttnArgs& a, const Parts& parts, cudaStream_t stream);
+int decode_rows(const AttnArgs& a, const Parts& parts, const UnitFlags& flags, cudaStream_t stream);
 
 }  // namespace paged
 }  // namespace wall

@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           s.slot = run.ta == 0 ? 1 : 0;
           if (lane == 0 && run.ta == 0 && !s.whole) {
             PartDesc d;
-            d.req = s.req; d.h = s.h; d.b = c.b;
+            d.t0 = c.r.t0 + c.b * BM; d.rows = min(BM, c.r.n - c.b * BM); d.h = s.h;
             d.last_cta = ending_cta(sh, c, x);
             parts.desc[cta] = d;
           }
@@ -985,9 +985,6 @@ bool chunk_rows_supported(int dtype, int K, int V) {
 
 int chunk_rows(const AttnArgs& a, const Parts& parts, const UnitFlags& flags, void* qh,
                cudaStream_t stream) {
-  if (cudaMemsetAsync(flags.f, 0, sizeof(int) * flags.count(a.bt.N, a.bt.T, a.HQ), stream) !=
-      cudaSuccess)
-    return WALL_ERR_CUDA;
   __nv_bfloat16* q16 = static_cast<__nv_bfloat16*>(qh);
   const int blocks = a.bt.T < kSms * 8 ? a.bt.T : kSms * 8;
   chunk_queries_kernel<<<blocks, 256, 0, stream>>>(a, q16, flags);

@@ -29,6 +29,8 @@ constexpr int kBox = kTile * 128;  // 64 channels of 32 rows
 
 struct DecodeLaunch {
   int G, stages, stage_bytes;
+  int* clear;  // words to clear, for the kernels behind this one
+  long clear_n;
 };
 
 template <int KD, int VD, int WPH>
@@ -56,6 +58,8 @@ __global__ void __launch_bounds__(288, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cta = blockIdx.x;
   const Pick pk = {1, 1};
+  for (long i = (long)cta * blockDim.x + threadIdx.x; i < dl.clear_n; i += (long)gridDim.x * blockDim.x)
+    dl.clear[i] = 0;
   if (threadIdx.x == 0) {
     parts.desc[cta].last_cta = -1;
     for (int st = 0; st < stages; ++st) {
@@ -341,7 +345,7 @@ __global__ void __launch_bounds__(288, 1)
             pm[1] = l;
             if (slot == 1 && g == 0) {
               PartDesc d;
-              d.req = c.r.i; d.h = kh; d.b = 0;
+              d.t0 = c.r.t0; d.rows = G; d.h = kh;
               d.last_cta = sh.last_owner<kUnit>(c, x);
               parts.desc[cta] = d;
             }
@@ -356,9 +360,11 @@ __global__ void __launch_bounds__(288, 1)
 }
 
 template <int KD, int VD, int WPH>
-int launch(const AttnArgs& a, const Parts& parts, cudaStream_t stream) {
+int launch(const AttnArgs& a, const Parts& parts, const UnitFlags& flags, cudaStream_t stream) {
   DecodeLaunch dl;
   dl.G = a.HQ / a.H;
+  dl.clear = flags.f;
+  dl.clear_n = flags.total;
   CUtensorMap tk, tv;
   if (!make_page_map(&tk, a.kp, (long)a.NP * a.HQ, 1 << a.shift, KD, kTile, dl.G) ||
       !make_page_map(&tv, a.vp, (long)a.NP * a.H, 1 << a.shift, VD, kTile, 1))
@@ -378,14 +384,14 @@ int launch(const AttnArgs& a, const Parts& parts, cudaStream_t stream) {
 }
 
 template <int KD, int VD>
-int launch_heads(const AttnArgs& a, const Parts& parts, cudaStream_t stream) {
+int launch_heads(const AttnArgs& a, const Parts& parts, const UnitFlags& flags, cudaStream_t stream) {
   // eight consumer warps where the head count lets them: fewer cannot keep up
   // with the copies
   const int G = a.HQ / a.H;
-  if (G == 1) return launch<KD, VD, 8>(a, parts, stream);
-  if (G == 2) return launch<KD, VD, 4>(a, parts, stream);
-  if (G <= 4) return launch<KD, VD, 2>(a, parts, stream);
-  return launch<KD, VD, 1>(a, parts, stream);
+  if (G == 1) return launch<KD, VD, 8>(a, parts, flags, stream);
+  if (G == 2) return launch<KD, VD, 4>(a, parts, flags, stream);
+  if (G <= 4) return launch<KD, VD, 2>(a, parts, flags, stream);
+  return launch<KD, VD, 1>(a, parts, flags, stream);
 }
 
 }  // namespace
@@ -396,11 +402,11 @@ bool decode_rows_supported(int dtype, int H, int HQ, int K, int V) {
   return dtype == WALL_BF16 && (K == 64 || K == 128) && (V == 64 || V == 128) && HQ / H <= 8;
 }
 
-int decode_rows(const AttnArgs& a, const Parts& parts, cudaStream_t stream) {
-  if (a.K == 128 && a.V == 128) return launch_heads<128, 128>(a, parts, stream);
-  if (a.K == 128) return launch_heads<128, 64>(a, parts, stream);
-  if (a.V == 128) return launch_heads<64, 128>(a, parts, stream);
-  return launch_heads<64, 64>(a, parts, stream);
+int decode_rows(const AttnArgs& a, const Parts& parts, const UnitFlags& flags, cudaStream_t stream) {
+  if (a.K == 128 && a.V == 128) return launch_heads<128, 128>(a, parts, flags, stream);
+  if (a.K == 128) return launch_heads<128, 64>(a, parts, flags, stream);
+  if (a.V == 128) return launch_heads<64, 128>(a, parts, flags, stream);
+  return launch_heads<64, 64>(a, parts, flags, stream);
 }
 
 }  // namespace paged
