@@ -23,6 +23,36 @@
 namespace wall {
 namespace paged {
 
+// Most of a call's kernels behind its first are launched while the one before
+// still runs (launch_behind): that one lets them start (start_next), and they
+// wait for it to have ended (wait_before) ahead of the first word that they
+// read of it, or write that it reads.  Every CTA waits, on every path, so that
+// the end of one means the end of all before it.  A call's first kernel is
+// launched in stream order: all of them may read the call's inputs at once.
+// Captured, single-token attention of three requests takes 10.3 us so instead
+// of 12.3, 160 draft rows 111 instead of 113; uncaptured, 112 instead of 123.
+__device__ __forceinline__ void start_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_before() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename... P, typename... A>
+int launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                  const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? WALL_OK : WALL_ERR_CUDA;
+}
+
 constexpr int kFrac = 24;
 constexpr float kOne = 16777216.f;                 // 2^24
 constexpr float kStep = 1.f / 16777216.f;          // 2^-24

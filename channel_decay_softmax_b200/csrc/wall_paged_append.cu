@@ -222,7 +222,10 @@ __global__ void __launch_bounds__(kWarps * 32, RL == 64 && sizeof(T) == 2 ? 4 : 
   bool none;
   if constexpr (kRuns) {
     const Run<RL> r = run_at<RL>(a.bt, blockIdx.x);
-    if (r.i < 0) return;
+    if (r.i < 0) {
+      wait_before();
+      return;
+    }
     i = r.i; t0 = r.t0; n = r.n; kv = r.kv; none = r.none; base = r.base;
   } else {
     i = blockIdx.x;
@@ -232,10 +235,14 @@ __global__ void __launch_bounds__(kWarps * 32, RL == 64 && sizeof(T) == 2 ? 4 : 
   }
   const int ctx = kv - n;
   if ((int)blockIdx.y >= a.k_slabs) {
-    if (none) return;
+    if (none) {
+      if constexpr (kRuns) wait_before();
+      return;
+    }
     const int ta = kRuns ? t0 + max(base, ctx) - ctx : t0;
     const int tb = kRuns ? t0 + min(base + RL, kv) - ctx : t0 + n;
     copy_values<T>(a, ta, tb, blockIdx.y - a.k_slabs);
+    if constexpr (kRuns) wait_before();
     return;
   }
   const int C = a.HQ * a.K;
@@ -244,6 +251,7 @@ __global__ void __launch_bounds__(kWarps * 32, RL == 64 && sizeof(T) == 2 ? 4 : 
   const int h = live ? c / a.K : 0, ch = live ? c - h * a.K : 0;
   const int PS1 = (1 << a.shift) - 1;
   if (none) {
+    if constexpr (kRuns) wait_before();
     if (live && grp == 0 && a.carry_out != a.carry_in) {
       long long x[4];
       load4(a.carry_in + (long)i * C + c, x);
@@ -258,8 +266,7 @@ __global__ void __launch_bounds__(kWarps * 32, RL == 64 && sizeof(T) == 2 ? 4 : 
   const int sc = blockIdx.y * kSlab + threadIdx.x;
   const bool scans = threadIdx.x < kSlab && sc < C;
   long long carry = 0;
-  if (scans && (kRuns || ctx > 0))
-    carry = kRuns ? a.runs[(long)blockIdx.x * C + sc] : a.carry_in[(long)i * C + sc];
+  if (!kRuns && scans && ctx > 0) carry = a.carry_in[(long)i * C + sc];
   bool wide = false, bad = false;
   for (;; base += RL) {
     const int o0 = base + grp * TPW;  // this group's first position
@@ -288,6 +295,10 @@ __global__ void __launch_bounds__(kWarps * 32, RL == 64 && sizeof(T) == 2 ? 4 : 
     if (po == o0)
       *reinterpret_cast<int4*>(&s_first[(o0 - base) >> 5][lane * 4]) =
           make_int4(step[0][0], step[0][1], step[0][2], step[0][3]);
+    if constexpr (kRuns) {
+      wait_before();
+      if (scans) carry = a.runs[(long)blockIdx.x * C + sc];
+    }
     __syncthreads();
     if (threadIdx.x < kSlab) {
 #pragma unroll 4
@@ -351,6 +362,7 @@ template <typename T, int RL>
 __global__ void __launch_bounds__(kWarps * 32) run_sums_kernel(AppendArgs a) {
   constexpr int TPW = RL / W;
   __shared__ __align__(16) long long s_sum[W][kSlab];
+  start_next();
   const int lane = threadIdx.x & 15, grp = threadIdx.x >> 4;
   const Run<RL> r = run_at<RL>(a.bt, blockIdx.x);
   if (r.i < 0 || r.none) return;
@@ -378,9 +390,11 @@ __global__ void __launch_bounds__(kWarps * 32) run_sums_kernel(AppendArgs a) {
 template <int RL>
 __global__ void __launch_bounds__(256) run_scan_kernel(AppendArgs a) {
   __shared__ long long s_part[8][32];
+  start_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = blockIdx.x, C = a.HQ * a.K, c = blockIdx.y * 32 + lane;
   const int t0 = a.bt.start(i), n = a.bt.rows(i), kv = a.bt.kv[i], ctx = kv - n;
+  wait_before();
   if (n == 0 || ctx < 0) return;
   const int count = (kv - 1) / RL - ctx / RL + 1;
   const int each = (count + 7) / 8, r0 = warp * each, r1 = min(count, r0 + each);
@@ -501,8 +515,9 @@ int append_tokens(AppendArgs& a, int max_new, int v_slabs, cudaStream_t stream) 
   } else {
     const int places = (int)run_places(a.bt.N, a.bt.T, a.shift);
     run_sums_kernel<T, RL><<<dim3(places, a.k_slabs), kWarps * 32, 0, stream>>>(a);
-    run_scan_kernel<RL><<<dim3(a.bt.N, ceil_div((long)a.HQ * a.K, 32)), 256, 0, stream>>>(a);
-    append_kernel<T, RL, true><<<dim3(places, slabs), kWarps * 32, 0, stream>>>(a);
+    if (launch_behind(run_scan_kernel<RL>, dim3(a.bt.N, ceil_div((long)a.HQ * a.K, 32)), 256, 0, stream, a) ||
+        launch_behind(append_kernel<T, RL, true>, dim3(places, slabs), kWarps * 32, 0, stream, a))
+      return WALL_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? WALL_OK : WALL_ERR_CUDA;
 }

@@ -228,6 +228,8 @@ __global__ void __launch_bounds__(kGenThreads, 3) general_kernel(AttnArgs a, Pic
   extern __shared__ __align__(16) float gen_shared[];
   __shared__ FindScratch fs;
   const int cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  start_next();
+  wait_before();
   if (threadIdx.x == 0) parts.desc[cta].last_cta = -1;
   Share sh;
   if (!find_start<GR, 0>(a.bt, a.window, a.HQ, pk, 1, cta, parts.n_cta, fs, sh)) return;
@@ -279,6 +281,7 @@ __global__ void __launch_bounds__(kGenThreads, 3) general_kernel(AttnArgs a, Pic
 template <typename T, int VPL>
 __global__ void __launch_bounds__(kGenThreads, 3) flagged_kernel(AttnArgs a, UnitFlags flags) {
   extern __shared__ __align__(16) float gen_shared[];
+  wait_before();
   if (*flags.any(a.HQ) == 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int at = 0;  // (block, head, quarter) items before the request
@@ -319,6 +322,8 @@ struct JoinSets {
 };
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(AttnArgs a, JoinSets sets) {
+  start_next();
+  wait_before();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool second = (int)blockIdx.x >= sets.s[0].parts.n_cta;
   const Parts parts = second ? sets.s[1].parts : sets.s[0].parts;
@@ -399,21 +404,25 @@ int join(const AttnArgs& a, const JoinSets& sets, cudaStream_t stream) {
     ctas += s.parts.n_cta;
     rows = std::max(rows, s.group > 0 ? s.group : s.parts.rows);
   }
-  join_kernel<T><<<dim3(ctas, std::min(kJoinY, ceil_div(rows, kJoinThreads / 32))), kJoinThreads, 0, stream>>>(a, sets);
-  return cudaGetLastError() == cudaSuccess ? WALL_OK : WALL_ERR_CUDA;
+  return launch_behind(join_kernel<T>, dim3(ctas, std::min(kJoinY, ceil_div(rows, kJoinThreads / 32))),
+                       kJoinThreads, 0, stream, a, sets);
 }
 
 template <typename T, int VPL>
-int launch_general(const AttnArgs& a, const Pick& pk, const Parts& parts, cudaStream_t stream) {
+int launch_general(const AttnArgs& a, const Pick& pk, const Parts& parts, bool first, cudaStream_t stream) {
   static bool attr[kMaxDevices] = {};
   if (!set_max_smem_once(general_kernel<T, VPL>, (int)gen_smem(128, 128), attr)) return WALL_ERR_CUDA;
-  general_kernel<T, VPL><<<parts.n_cta, kGenThreads, gen_smem(a.K, a.V), stream>>>(a, pk, parts);
-  return cudaGetLastError() == cudaSuccess ? WALL_OK : WALL_ERR_CUDA;
+  if (first) {
+    general_kernel<T, VPL><<<parts.n_cta, kGenThreads, gen_smem(a.K, a.V), stream>>>(a, pk, parts);
+    return cudaGetLastError() == cudaSuccess ? WALL_OK : WALL_ERR_CUDA;
+  }
+  return launch_behind(general_kernel<T, VPL>, parts.n_cta, kGenThreads, gen_smem(a.K, a.V), stream, a,
+                       pk, parts);
 }
 template <typename T>
-int run_general(const AttnArgs& a, const Pick& pk, const Parts& parts, cudaStream_t stream) {
-  return a.V <= 64 ? launch_general<T, 2>(a, pk, parts, stream)
-                   : launch_general<T, 4>(a, pk, parts, stream);
+int run_general(const AttnArgs& a, const Pick& pk, const Parts& parts, bool first, cudaStream_t stream) {
+  return a.V <= 64 ? launch_general<T, 2>(a, pk, parts, first, stream)
+                   : launch_general<T, 4>(a, pk, parts, first, stream);
 }
 
 size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -423,8 +432,8 @@ int launch_flagged(const AttnArgs& a, const UnitFlags& flags, cudaStream_t strea
   using T = __nv_bfloat16;
   static bool attr[kMaxDevices] = {};
   if (!set_max_smem_once(flagged_kernel<T, VPL>, (int)gen_smem(128, 128), attr)) return WALL_ERR_CUDA;
-  flagged_kernel<T, VPL><<<kGeneralCtas, kGenThreads, gen_smem(a.K, a.V), stream>>>(a, flags);
-  return cudaGetLastError() == cudaSuccess ? WALL_OK : WALL_ERR_CUDA;
+  return launch_behind(flagged_kernel<T, VPL>, kGeneralCtas, kGenThreads, gen_smem(a.K, a.V), stream, a,
+                       flags);
 }
 int run_flagged(const AttnArgs& a, const UnitFlags& flags, cudaStream_t stream) {
   return a.V <= 64 ? launch_flagged<2>(a, flags, stream) : launch_flagged<4>(a, flags, stream);
@@ -526,8 +535,8 @@ int paged_attn(const PagedAttnProblem& pb, void* ws, cudaStream_t stream) {
   }
   if (r.general) {
     const Parts p = parts_at(ws, w.gen_desc, w.gen_data, GR, kGeneralCtas);
-    const int rc = pb.dtype == WALL_BF16 ? run_general<__nv_bfloat16>(a, r.rows, p, stream)
-                                         : run_general<float>(a, r.rows, p, stream);
+    const int rc = pb.dtype == WALL_BF16 ? run_general<__nv_bfloat16>(a, r.rows, p, sets.n == 0, stream)
+                                         : run_general<float>(a, r.rows, p, sets.n == 0, stream);
     if (rc) return rc;
     sets.s[sets.n++] = {p, 0};
   }

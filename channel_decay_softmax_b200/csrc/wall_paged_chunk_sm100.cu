@@ -282,9 +282,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     fence_barrier_init();
   }
+  start_next();
   Share sh;
   long long x0, x1;
-  if (!start_share(a.bt, a.window, a.HQ, cta, parts.n_cta, fs, sh, x0, x1)) return;
+  if (!start_share(a.bt, a.window, a.HQ, cta, parts.n_cta, fs, sh, x0, x1)) {
+    wait_before();
+    return;
+  }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_holder), 512);
     tmem_relinquish();
@@ -293,6 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  wait_before();
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA
@@ -914,6 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // flags the row's unit.
 __global__ void __launch_bounds__(256) chunk_queries_kernel(AttnArgs a, __nv_bfloat16* qh,
                                                             UnitFlags flags) {
+  start_next();
   const int per_row = a.HQ * a.K / 8;
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
   for (int t = blockIdx.x; t < a.bt.T; t += gridDim.x) {
@@ -970,9 +976,8 @@ int launch(const AttnArgs& a, const Parts& parts, const UnitFlags& flags, __nv_b
     return WALL_ERR_CUDA;
   static bool attr[kMaxDevices] = {};
   if (!set_max_smem_once(paged_chunk_kernel<KD>, Smem<KD>::kAlloc, attr)) return WALL_ERR_CUDA;
-  paged_chunk_kernel<KD><<<parts.n_cta, kThreads, Smem<KD>::kAlloc, stream>>>(tq, tk, tv, a, parts,
-                                                                             flags);
-  return cudaGetLastError() == cudaSuccess ? WALL_OK : WALL_ERR_CUDA;
+  return launch_behind(paged_chunk_kernel<KD>, parts.n_cta, kThreads, Smem<KD>::kAlloc, stream, tq, tk,
+                       tv, a, parts, flags);
 }
 
 }  // namespace
@@ -987,6 +992,9 @@ int chunk_rows(const AttnArgs& a, const Parts& parts, const UnitFlags& flags, vo
                cudaStream_t stream) {
   __nv_bfloat16* q16 = static_cast<__nv_bfloat16*>(qh);
   const int blocks = a.bt.T < kSms * 8 ? a.bt.T : kSms * 8;
+  // In stream order: started while the decode kernel holds the SMs' shared
+  // memory, it would run with the L1 that this leaves (an 8192-token prompt:
+  // 416 us for the call against 406).
   chunk_queries_kernel<<<blocks, 256, 0, stream>>>(a, q16, flags);
   if (cudaGetLastError() != cudaSuccess) return WALL_ERR_CUDA;
   return a.K == 128 ? launch<128>(a, parts, flags, q16, stream)

@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(288, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cta = blockIdx.x;
   const Pick pk = {1, 1};
+  start_next();
   for (long i = (long)cta * blockDim.x + threadIdx.x; i < dl.clear_n; i += (long)gridDim.x * blockDim.x)
     dl.clear[i] = 0;
   if (threadIdx.x == 0) {

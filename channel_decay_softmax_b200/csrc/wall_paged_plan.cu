@@ -72,6 +72,7 @@ __device__ __forceinline__ void write_slot(const PlanArgs& a, int t, int lo, int
 // the admitted requests' pages are the top of the stack, in request order.
 __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanArgs a, int slots_here) {
   __shared__ long long sw[32];
+  start_next();
   const int lane = threadIdx.x & 31;
   const int PS1 = (1 << a.shift) - 1;
   int n_free = *a.free_count;
@@ -148,6 +149,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanArgs a, int s
 constexpr int kSlotRows = 1024, kSlotThreads = 256;
 __global__ void __launch_bounds__(kSlotThreads) slots_kernel(PlanArgs a) {
   __shared__ int s_lo, s_hi;
+  wait_before();
   const int t0 = blockIdx.x * kSlotRows, t1 = min(t0 + kSlotRows, a.T);
   if (threadIdx.x == 0) s_lo = s_hi = 0;
   __syncthreads();
@@ -221,8 +223,9 @@ int paged_plan(const int* new_lens, const int* lens, int* table, const int* free
   a.lens_out = lens_out; a.free_out = free_out; a.status = device_status();
   const bool here = T <= kSlotsHere || N == 0;
   plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, here ? 1 : 0);
-  if (!here) slots_kernel<<<(T + kSlotRows - 1) / kSlotRows, kSlotThreads, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? WALL_OK : WALL_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return WALL_ERR_CUDA;
+  if (here) return WALL_OK;
+  return launch_behind(slots_kernel, (T + kSlotRows - 1) / kSlotRows, kSlotThreads, 0, stream, a);
 }
 
 int paged_release(const int* finished, int* lens, int* table, int* free_list, int* free_count,
