@@ -15,6 +15,8 @@
 namespace wall {
 namespace {
 
+using namespace paged;
+
 constexpr int kPlanThreads = 1024;
 
 struct PlanArgs {
