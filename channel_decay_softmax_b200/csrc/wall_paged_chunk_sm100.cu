@@ -10,9 +10,9 @@
 // key tile is exact: Qh is the only operand that is rounded (to bf16, half a
 // step of 2^-8, as a tensor-core operand has to be).  P is rounded to bf16
 // for P V; its sum is taken in fp32 before that.  A unit whose exponents pass
-// +-100 on some channel, or whose partly masked tiles hold a value that is not
-// finite (it would reach the masked rows as 0 * inf), is flagged, and the
-// general kernel computes it again, exactly, behind this one.
+// +-100 on some channel, or whose result holds a NaN (a value that is not finite
+// reaches the rows that do not see it as 0 * inf), is flagged, and the general
+// kernel computes it again, exactly, behind this one.
 //
 // Work.  One CTA per SM takes an even share of the batch's (unit, 128-key
 // tile) pairs in order (wall_paged.cuh): the tile pipeline's rings and
@@ -26,9 +26,9 @@
 //               the key ring (3 stages, with the pages' anchors), the value
 //               ring (2 stages), the units' Qh
 //   warp 1      TMEM owner and MMA issuer (one thread)
-//   warps 2-3   key rescale in place; partly masked tiles: value rows past the
-//               request's end zeroed (pages end inside tiles; what they hold
-//               there is another request's, or nothing), the others checked
+//   warps 2-3   key rescale in place; zeros in place of the value rows past a
+//               request's last key (pages end inside tiles; what they hold
+//               there is an earlier request's, or nothing)
 //   warps 4-7   softmax of the CTA's even tiles, warps 8-11 of its odd ones:
 //               one query row a thread, the two groups' (m, l, O) merged at a
 //               unit's end
@@ -126,7 +126,7 @@ enum Bar {
   B_KEMPTY = B_KREADY + kKS,    // + key stage
   B_VFULL = B_KEMPTY + kKS,     // + value stage: ready for P V (2 arrivals)
   B_VEMPTY = B_VFULL + kVS,     // + value stage
-  B_VRAW = B_VEMPTY + kVS,      // + value stage: a partly masked tile has landed
+  B_VRAW = B_VEMPTY + kVS,      // + value stage: a tile that the keys end in has landed
   B_SFULL = B_VRAW + kVS,       // + S buffer (2)
   B_PFULL = B_SFULL + 2,        // + group (2), 4 warps each
   B_PVDONE = B_PFULL + 2,       // + group (2)
@@ -205,33 +205,18 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_l
       "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(keep), "r"(kDescHi));
 }
 
-// Any half of the word that is an infinity or a NaN
-__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
-  return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-}
-
-// A value tile of which nk rows are keys, by the 64 threads of the rescale
-// warps: the other rows become zeros; returns whether this thread saw a value
-// that is not finite among the keys'.
+// Zeros in place of a value tile's rows from nk on, by the 64 threads of the
+// rescale warps.
 template <int KD>
-__device__ __noinline__ bool clear_and_check(uint8_t* tile, int nk) {
+__device__ __noinline__ void clear_rows(uint8_t* tile, int nk) {
   constexpr int kChunks = KD / 8, kRowStep = 64 / kChunks;
   const int tid = threadIdx.x - 64, ch = tid % kChunks;
   uint8_t* vt = tile + (ch / 8) * (BN * 128);
-  uint32_t bad = 0;
 #pragma unroll 4
-  for (int r = tid / kChunks; r < BN; r += kRowStep) {
-    uint4* w = reinterpret_cast<uint4*>(vt + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
-    if (r >= nk) {
-      *w = make_uint4(0u, 0u, 0u, 0u);
-    } else {
-      const uint4 x = *w;
-      bad |= not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w);
-    }
-  }
+  for (int r = nk + tid / kChunks; r < BN; r += kRowStep)
+    *reinterpret_cast<uint4*>(vt + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   __syncwarp();
-  return bad != 0;
 }
 
 template <int KD>
@@ -408,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int left_v = 0, y_v = 0, seg_v = -1;
     int slot_v = 0, ids_v = 0;
     int k_out = 0, v_out = 0, q_out = 0;
-    uint32_t raw = 0, raw_next = 0;     // per value stage: its last tile is a partly masked one;
+    uint32_t raw = 0, raw_next = 0;     // per value stage: the keys end in its last tile;
                                         // parity of the next one's B_VRAW phase
     bool more = true;                   // key tiles
     for (int g = 0;; ++g) {
@@ -446,9 +431,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int st = (g - 2) % kVS;
         if (g - 2 >= kVS && !waits(B_VEMPTY + st, (g - 2) / kVS - 1)) break;
         const Segment& s = segs[seg_v % kSegs];
-        // a partly masked tile goes to the rescale warps first, which then
-        // make the two arrivals on B_VFULL
-        const bool part = y_v < s.fa || y_v >= s.fb;
+        // a tile that the request's last key ends in goes to the rescale warps
+        // first, which then make the two arrivals on B_VFULL
+        const bool part = s.kv - (s.j0 + y_v * BN) < BN;
         if (part) {
           raw |= 1u << st;
           raw_next ^= 1u << st;
@@ -563,19 +548,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ch = tid % kChunks;
     const int rs = tid / kChunks;
     const int PS = 1 << a.shift;
-    uint32_t raw = 0;  // parity of each value stage's next partly masked tile
+    uint32_t raw = 0;  // parity of each value stage's next B_VRAW phase
     int g = 0;
     bool ok = true;
-    auto check_values = [&](int gv, int nk, int unit) {
+    auto end_values = [&](int gv, int nk) {
       const int vs = gv % kVS;
       if (!__all_sync(0xffffffffu, wait_bar(bar(B_VRAW + vs), (raw >> vs) & 1u, a.status, abort_flag)))
         return false;
       raw ^= 1u << vs;
-      if (clear_and_check<KD>(smem + Lay::oV + vs * Lay::kT, nk)) flags.set(unit, a.HQ);
+      clear_rows<KD>(smem + Lay::oV + vs * Lay::kT, nk);
       if (lane == 0) mbar_arrive(bar(B_VFULL + vs));
       return true;
     };
-    int nk1 = -1, nk2 = -1, unit1 = 0, unit2 = 0;  // the last two tiles' (-1: seen whole)
+    int nk1 = -1, nk2 = -1;  // keys of the last two tiles (-1: all)
     for (int seg = 0; ok; ++seg) {
       if (!__all_sync(0xffffffffu, wait_bar(bar(B_SEG + seg % kSegs), (seg / kSegs) & 1, a.status,
                                             abort_flag)))
@@ -650,24 +635,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_KREADY + st));
-        // The value tile of two tiles ago, where it is partly masked: by now it
+        // The value tile of two tiles ago, where the keys end in it: by now it
         // has landed, and the keys that the next S need are scaled already.
-        if (nk2 >= 0 && !check_values(g - 2, nk2, unit2)) {
+        if (nk2 >= 0 && !end_values(g - 2, nk2)) {
           ok = false;
           break;
         }
         nk2 = nk1;
-        unit2 = unit1;
-        nk1 = y < s.fa || y >= s.fb ? max(0, min(BN, s.kv - j0)) : -1;
-        unit1 = s.place * a.HQ + s.h;
+        nk1 = s.kv - j0 < BN ? max(0, s.kv - j0) : -1;
       }
       if (flag) flags.set(s.place * a.HQ + s.h, a.HQ);
     }
 #pragma unroll 1
     for (int left = 2; ok && left > 0; --left) {
-      if (nk2 >= 0) ok = check_values(g - left, nk2, unit2);
+      if (nk2 >= 0) ok = end_values(g - left, nk2);
       nk2 = nk1;
-      unit2 = unit1;
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -855,6 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long row = (long)(s.t0 + r) * a.HQ + h;
         // each group writes half of the channels
         if (!idle) {
+          bool bad = false;  // a NaN: perhaps 0 * infinity or 0 * NaN of a masked value
 #pragma unroll 1
           for (int cc = grp * (V / 2); cc < (grp + 1) * (V / 2); cc += 32) {
             uint32_t ov0[32], ov1[32];
@@ -866,6 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               // (a row whose weight is 0 had no key in the group: its O is 0)
               float x = has0 ? __uint_as_float(ov0[e]) * f0 : 0.f;
               if (has1) x = fmaf(__uint_as_float(ov1[e]), f1, x);
+              bad |= x != x;
               ov0[e] = __float_as_uint(x);
             }
             if (row_ok) {
@@ -889,6 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           tc_fence_before();
+          if (bad && row_ok) flags.set(s.place * a.HQ + h, a.HQ);
         }
         if (grp == 0 && row_ok) {
           if (whole) {
