@@ -8,7 +8,10 @@
 // 64 channels x 32 rows x G heads per 128 bytes of key row -- the pages are
 // head-major, so each head's piece is contiguous -- the value boxes and the
 // page's anchors), and the tile's G heads have WPH warps each that take
-// alternate tiles with a softmax state of their own: lane = key for the
+// alternate stages with a softmax state of their own (a stage is the same
+// warp's in every round, the stages being a multiple of WPH: a wait on a
+// barrier's parity tells a phase only from the one before, which its waiter
+// has to have seen): lane = key for the
 // scores, then lane = VD / 32 value channels for P V.  The share runs across
 // requests and heads, so the ring never drains between them, and a batch of
 // any lengths loads every SM alike.
@@ -26,6 +29,7 @@ using namespace paged;
 constexpr int kTile = 32;
 constexpr int kUnit = 1;           // a unit's own cost, in tiles
 constexpr int kBox = kTile * 128;  // 64 channels of 32 rows
+constexpr int kMaxStages = 16;
 
 struct DecodeLaunch {
   int G, stages, stage_bytes;
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(288, 1)
           st = 0;
           phase ^= 1;
         }
-        if (!ok || (t - ta) % WPH != par) continue;  // another warp's tile
+        if (!ok || cs % WPH != par) continue;  // another warp's stage
         {
           const bool got = mbar_wait(full(cs), cp, a.status);
           if (!__all_sync(0xffffffffu, got)) {
@@ -373,9 +377,10 @@ int launch(const AttnArgs& a, const Parts& parts, const UnitFlags& flags, cudaSt
   const int oR = (dl.G * (KD / 64) + VD / 64) * kBox;
   dl.stage_bytes = (oR + dl.G * KD * 4 + 1023) & ~1023;
   const int tail = dl.G * WPH * KD * 4 + dl.G * (WPH - 1) * 32 * (VD / 32 + 2) * 4 +
-                   (2 * 12 + 2 * dl.G) * 8;
+                   (2 * kMaxStages + 2 * dl.G) * 8;
   dl.stages = (226 * 1024 - 1024 - tail) / dl.stage_bytes;
-  if (dl.stages > 12) dl.stages = 12;
+  if (dl.stages > kMaxStages) dl.stages = kMaxStages;
+  dl.stages -= dl.stages % WPH;
   const int smem = dl.stages * dl.stage_bytes + tail + 1024;
   static bool attr[kMaxDevices] = {};
   if (!set_max_smem_once(paged_decode_kernel<KD, VD, WPH>, 226 * 1024, attr)) return WALL_ERR_CUDA;

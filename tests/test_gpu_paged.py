@@ -387,6 +387,21 @@ def test_attn_decode(HQ, H, K, V, dt, PS):
                sink=PS == 64, poison=True)
 
 
+@pytest.mark.parametrize("HQ,H", [(1, 1), (2, 1), (4, 1), (8, 2)])
+def test_attn_decode_keeps_its_order_of_tiles(HQ, H):
+    """Requests of one tile between requests of many, over and over: warps that
+    have no tile of a request must not run ahead of those that have, and every
+    run gives the same bits."""
+    ctx = [int(c) for c in np.random.default_rng(HQ).choice([0, 20, 70, 250, 500, 1500], 240)]
+    x, o, lse = _attn_case(HQ, H, 128, 128, 64, BF, [1] * len(ctx), ctx, hint=True)
+    cu, kv, table, _, _ = _batch([1] * len(ctx), ctx, 64, 0)
+    for _ in range(30):
+        again = api.wall_paged_attn(x["q"], x["p"], _i32(cu), _i32(kv), _i32(table), x["k_pages"],
+                                    x["v_pages"], x["r_pages"], max_new=1, scale=128 ** -0.5)
+        assert torch.equal(again, o)
+    _status_ok()
+
+
 @pytest.mark.parametrize("HQ,H,K,V,dt", SHAPES)
 @pytest.mark.parametrize("new,ctx", [
     ([2, 5], [0, 100]), ([33, 1, 64], [0, 40, 95]), ([129], [0]), ([40, 128, 1, 0, 130], [90, 128, 200, 7, 1])])
