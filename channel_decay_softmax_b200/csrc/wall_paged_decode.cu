@@ -11,11 +11,22 @@
 // alternate stages with a softmax state of their own (a stage is the same
 // warp's in every round, the stages being a multiple of WPH: a wait on a
 // barrier's parity tells a phase only from the one before, which its waiter
-// has to have seen): lane = key for the
-// scores, then lane = VD / 32 value channels for P V.  The share runs across
+// has to have seen).  The share runs across
 // requests and heads, so the ring never drains between them, and a batch of
 // any lengths loads every SM alike.
+//
+// A single row gives the tensor cores nothing to reuse, but as warp-level
+// matrix products (m16n8k16: 16 keys, or 16 value channels, by 8 columns)
+// the two contractions take a quarter of the instructions of fp32 FMAs, which
+// unpack every element first and bound this kernel by issue and power (32
+// requests of up to 131072 tokens: 525 us cold, 601 us at the 1000 W limit).
+// The 8 columns hold the one vector's parts: q 2^(...) as a sum of three
+// bf16 (24 bits: nothing of the fp32 value is lost) and P as a sum of two (to
+// 2^-16, beside the output's rounding of 2^-8; its sum is taken in fp32
+// before that), so that products are exact and sums are fp32.
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "sm100_ptx.cuh"
 #include "wall_paged_attn.h"
@@ -30,6 +41,37 @@ constexpr int kTile = 32;
 constexpr int kUnit = 1;           // a unit's own cost, in tiles
 constexpr int kBox = kTile * 128;  // 64 channels of 32 rows
 constexpr int kMaxStages = 16;
+
+// A query's operand in shared memory: per (lane & 3, part) the words of its
+// k-steps, 80 bytes apart so that a warp's vector reads meet few banks twice
+constexpr int kQGroup = 80, kQBytes = 12 * kQGroup;
+
+__device__ __forceinline__ void ldsm4(uint32_t (&d)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&d)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// two floats to bf16, the first in the low half
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+__device__ __forceinline__ float low_of(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// what a bf16 part leaves of a value; of an infinity nothing
+__device__ __forceinline__ float rest_of(float x, float part) {
+  return fabsf(part) == INFINITY ? 0.f : x - part;
+}
 
 struct DecodeLaunch {
   int G, stages, stage_bytes;
@@ -52,9 +94,9 @@ __global__ void __launch_bounds__(288, 1)
   const int oV = G * (KD / 64) * kBox;               // within a stage
   const int oR = oV + (VD / 64) * kBox;              // anchors int32 [G][KD]
   const int nw = G * WPH;                            // consumer warps
-  float* qts = reinterpret_cast<float*>(smem + stages * dl.stage_bytes);  // [nw][KD]
-  float* xch = qts + nw * KD;                        // [G][WPH - 1][32][VPL + 2]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(xch + G * (WPH - 1) * 32 * (VPL + 2));
+  uint8_t* qts = smem + stages * dl.stage_bytes;     // [nw] query operands
+  float* xch = reinterpret_cast<float*>(qts + nw * kQBytes);  // [G][WPH][VD + 4]: sums, m, l
+  uint64_t* bars = reinterpret_cast<uint64_t*>(xch + nw * (VD + 4));
   auto full = [&](int st) { return smem_u32(&bars[st]); };
   auto empty = [&](int st) { return smem_u32(&bars[stages + st]); };
   auto xfull = [&](int g) { return smem_u32(&bars[2 * stages + g]); };
@@ -147,7 +189,17 @@ __global__ void __launch_bounds__(288, 1)
     // ------------------------------------------------------------ query heads
     const int g = warp % G, par = warp / G;
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-    float* qt = qts + warp * KD;
+    uint8_t* qt = qts + warp * kQBytes;
+    // this lane's place among the fragments: row or column lane / 4, pair lane % 4
+    const int quad = lane >> 2, pr4 = lane & 3;
+    // columns 2j hold the first part, odd ones the second and third in turns
+    const int part = (quad & 1) == 0 ? 0 : (quad & 2) == 0 ? 1 : 2;
+    // ldmatrix rows: of a key tile (keys, then channels on), of a value tile
+    // (channels, then keys on); both 128-byte rows with the 128-byte swizzle
+    const int sw = lane & 7;
+    const uint32_t krow = (sw + ((lane >> 3) & 1) * 8) * 128, kch = lane >> 4;
+    const uint32_t vrow = (sw + (lane >> 4) * 8) * 128, vch = (lane >> 3) & 1;
+    uint32_t qb[KD / 8];  // the query's fragments, two words a k-step
     const int win = a.window > 0 ? a.window : 0x7fffffff;
     int st = 0;           // stage and phase of the CTA's next tile
     uint32_t phase = 0;
@@ -180,9 +232,12 @@ __global__ void __launch_bounds__(288, 1)
           Rq[y] = page >= 0 ? a.rp[((long)page * a.HQ + h) * KD + lane * QPL + y] : 0;
         }
       }
-      float m = -INFINITY, l = 0.f, acc[VPL];
+      float m = -INFINITY, l = 0.f;
+      float acc[VD / 16][4];  // channels 16 c + quad (parts 0, 1) and + 8
 #pragma unroll
-      for (int y = 0; y < VPL; ++y) acc[y] = 0.f;
+      for (int y = 0; y < VD / 16; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[y][e] = 0.f;
       int page_at = -1;
       for (int t = ta; t < tb; ++t) {
         const int cs = st;
@@ -202,126 +257,166 @@ __global__ void __launch_bounds__(288, 1)
         const uint8_t* sb = smem + cs * dl.stage_bytes;
         const int j0 = (lo_tile + t) * kTile;
         if ((j0 >> a.shift) != page_at) {
-          // the query against this page: scale * log2(e) * q * 2^(p + R - R_c)
+          // the query against this page: scale * log2(e) * q * 2^(p + R - R_c),
+          // its three parts to the words that the fragments read
           const int* R = reinterpret_cast<const int*>(sb + oR) + g * KD + lane * QPL;
           __syncwarp();
 #pragma unroll
-          for (int y = 0; y < QPL; ++y) qt[lane * QPL + y] = qv[y] * exp2f(pv[y] + (float)(Rq[y] - R[y]));
+          for (int y = 0; y < QPL; y += 2) {
+            float x0 = qv[y] * exp2f(pv[y] + (float)(Rq[y] - R[y]));
+            float x1 = qv[y + 1] * exp2f(pv[y + 1] + (float)(Rq[y + 1] - R[y + 1]));
+            const int ch = lane * QPL + y, pair = (ch & 15) >> 1;
+            uint8_t* w = qt + (pair & 3) * 3 * kQGroup + ((ch >> 4) * 2 + (pair >> 2)) * 4;
+#pragma unroll
+            for (int z = 0; z < 3; ++z) {
+              const uint32_t h = pack2(x0, x1);
+              *reinterpret_cast<uint32_t*>(w + z * kQGroup) = h;
+              x0 = rest_of(x0, low_of(h));
+              x1 = rest_of(x1, high_of(h));
+            }
+          }
           __syncwarp();
+#pragma unroll
+          for (int y = 0; y < KD / 8; y += 4) {
+            const uint4 u = *reinterpret_cast<const uint4*>(qt + (pr4 * 3 + part) * kQGroup + y * 4);
+            qb[y] = u.x; qb[y + 1] = u.y; qb[y + 2] = u.z; qb[y + 3] = u.w;
+          }
           page_at = j0 >> a.shift;
         }
-        float d4[4] = {0.f, 0.f, 0.f, 0.f};
+        // scores of keys quad + 8 i: 16 keys an instruction
+        float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        const uint32_t kb = smem_u32(sb) + g * kBox + krow;
 #pragma unroll
-        for (int bx = 0; bx < KD / 64; ++bx) {
-          const uint8_t* krow = sb + (bx * G + g) * kBox + lane * 128;
+        for (int ks = 0; ks < KD / 16; ++ks) {
+          const uint32_t at = kb + (ks / 4) * G * kBox + ((((ks & 3) * 2 + kch) ^ sw) << 4);
 #pragma unroll
-          for (int c8 = 0; c8 < 8; ++c8) {
-            const uint4 u = *reinterpret_cast<const uint4*>(krow + ((c8 ^ (lane & 7)) << 4));
-            const float4 qa = *reinterpret_cast<const float4*>(qt + bx * 64 + c8 * 8);
-            const float4 qb = *reinterpret_cast<const float4*>(qt + bx * 64 + c8 * 8 + 4);
-            const __nv_bfloat162* hv = reinterpret_cast<const __nv_bfloat162*>(&u);
-            const float2 f0 = __bfloat1622float2(hv[0]), f1 = __bfloat1622float2(hv[1]);
-            const float2 f2 = __bfloat1622float2(hv[2]), f3 = __bfloat1622float2(hv[3]);
-            d4[0] = fmaf(f0.x, qa.x, d4[0]); d4[1] = fmaf(f0.y, qa.y, d4[1]);
-            d4[2] = fmaf(f1.x, qa.z, d4[2]); d4[3] = fmaf(f1.y, qa.w, d4[3]);
-            d4[0] = fmaf(f2.x, qb.x, d4[0]); d4[1] = fmaf(f2.y, qb.y, d4[1]);
-            d4[2] = fmaf(f3.x, qb.z, d4[2]); d4[3] = fmaf(f3.y, qb.w, d4[3]);
+          for (int y = 0; y < 2; ++y) {
+            uint32_t ka[4];
+            ldsm4(ka, at + y * 16 * 128);
+            mma16816(d[y], ka, qb[ks * 2], qb[ks * 2 + 1]);
           }
         }
-        const int j = j0 + lane;
-        const bool vis = !c.r.dead && j <= pos && j >= lo_key;
-        const float s = vis ? (d4[0] + d4[1]) + (d4[2] + d4[3]) : -INFINITY;
-        float mt = s;
+        const int ja = max(0, lo_key - j0), jb = c.r.dead ? 0 : min(kTile, pos + 1 - j0);
+        float sc[4], mt = -INFINITY;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-        const float m_new = fmaxf(m, mt);
-        const float use = m_new == -INFINITY ? 0.f : m_new;
-        const float alpha = exp2f(m - use);
-        const float pr = vis ? exp2f(s - use) : 0.f;
-        float ps = pr;
+        for (int y = 0; y < 4; ++y) {
+          const float lo = d[y >> 1][(y & 1) * 2 + 1];
+          sc[y] = d[y >> 1][(y & 1) * 2] + (lo + __shfl_xor_sync(0xffffffffu, lo, 1));
+          const int j = quad + 8 * y;
+          if (j < ja || j >= jb) sc[y] = -INFINITY;
+          mt = fmaxf(mt, sc[y]);
+        }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
-        l = l * alpha + ps;
-        m = m_new;
+        for (int o = 16; o > 2; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+        if (mt > m) {  // the same for the whole warp
+          const float alpha = exp2f(m - mt);
+          l *= alpha;
 #pragma unroll
-        for (int y = 0; y < VPL; ++y) acc[y] *= alpha;
-        // P V over the visible keys alone: what the other rows of the page
-        // hold (NaN included) does not enter
-        const int vbx = (lane * VPL) / 64, vch = (lane * VPL) % 64;
-        const uint8_t* vbase = sb + oV + vbx * kBox + (vch % 8) * 2;
-        auto add_key = [&](int jj) {
-          const float pj = __shfl_sync(0xffffffffu, pr, jj);
-          const uint8_t* vp = vbase + jj * 128 + (((vch / 8) ^ (jj & 7)) << 4);
-          if constexpr (VPL == 4) {
-            const uint2 u = *reinterpret_cast<const uint2*>(vp);
-            const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-            const float2 f1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-            acc[0] = fmaf(pj, f0.x, acc[0]); acc[1] = fmaf(pj, f0.y, acc[1]);
-            acc[2] = fmaf(pj, f1.x, acc[2]); acc[3] = fmaf(pj, f1.y, acc[3]);
-          } else {
-            const uint32_t u = *reinterpret_cast<const uint32_t*>(vp);
-            const float2 f0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
-            acc[0] = fmaf(pj, f0.x, acc[0]); acc[1] = fmaf(pj, f0.y, acc[1]);
+          for (int y = 0; y < VD / 16; ++y)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[y][e] *= alpha;
+          m = mt;
+        }
+        const float use = m == -INFINITY ? 0.f : m;
+        float p[4], ps = 0.f;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int j = quad + 8 * y;
+          p[y] = j < ja || j >= jb ? 0.f : exp2f(sc[y] - use);
+          ps += p[y];
+        }
+#pragma unroll
+        for (int o = 16; o > 2; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
+        l += ps;
+        // P V.  Of the keys that the row does not see the values count as 0:
+        // what those rows of the page hold (NaN included) does not enter.
+        const uint32_t vb = smem_u32(sb) + oV + vrow;
+        auto add_values = [&](auto all) {
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            uint32_t pb[2], keep[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float e0 = __shfl_sync(0xffffffffu, p[ks * 2 + y], pr4 * 8);
+              const float e1 = __shfl_sync(0xffffffffu, p[ks * 2 + y], pr4 * 8 + 4);
+              const uint32_t h = pack2(e0, e1);
+              pb[y] = (quad & 1) == 0 ? h : pack2(e0 - low_of(h), e1 - high_of(h));
+              const int j = ks * 16 + y * 8 + pr4 * 2;
+              keep[y] = (j >= ja && j < jb ? 0xffffu : 0u) | (j + 1 >= ja && j + 1 < jb ? 0xffff0000u : 0u);
+            }
+#pragma unroll
+            for (int y = 0; y < VD / 16; ++y) {
+              uint32_t va[4];
+              ldsm4_t(va, vb + (y / 4) * kBox + ks * 16 * 128 + ((((y & 3) * 2 + vch) ^ sw) << 4));
+              if constexpr (!decltype(all)::value) {
+                va[0] &= keep[0];
+                va[1] &= keep[0];
+                va[2] &= keep[1];
+                va[3] &= keep[1];
+              }
+              mma16816(acc[y], va, pb[0], pb[1]);
+            }
           }
         };
-        const int ja = max(0, lo_key - j0), jb = c.r.dead ? 0 : min(kTile, pos + 1 - j0);
-        if (ja == 0 && jb == kTile) {
-#pragma unroll
-          for (int jj = 0; jj < kTile; ++jj) add_key(jj);
-        } else {
-          for (int jj = ja; jj < jb; ++jj) add_key(jj);
-        }
+        if (ja == 0 && jb == kTile) add_values(std::true_type{});
+        else add_values(std::false_type{});
         __syncwarp();
         if (lane == 0) mbar_arrive(empty(cs));
       }
-      // the head's warps meet: the others hand their states to the first
+      // The head's warps meet: each lays its state into shared memory in the
+      // channels' order, and the first joins them.
       if (!__all_sync(0xffffffffu, ok)) ok = false;
-      if constexpr (WPH > 1) {
-        float* xs = xch + ((g * (WPH - 1)) * 32 + lane) * (VPL + 2);
-        if (par > 0) {
-          const bool got = n_seg == 0 || mbar_wait(xempty(g), (uint32_t)((n_seg - 1) & 1), a.status);
-          float* mine = xs + (par - 1) * 32 * (VPL + 2);
-          if (got) {
+      float* xs = xch + g * WPH * (VD + 4);
+      if (par > 0 && n_seg > 0 && !__all_sync(0xffffffffu, mbar_wait(xempty(g), (uint32_t)((n_seg - 1) & 1),
+                                                                     a.status)))
+        ok = false;  // (its state is not laid down, nor announced)
+      else {
+        float* mine = xs + par * (VD + 4);
 #pragma unroll
-            for (int y = 0; y < VPL; ++y) mine[y] = acc[y];
-            mine[VPL] = ok ? m : -INFINITY;  // a part that lacks tiles counts as empty
-            mine[VPL + 1] = ok ? l : 0.f;
-          }
-          __syncwarp();
-          if (lane == 0 && got) mbar_arrive(xfull(g));
-        } else {
-          const bool got = mbar_wait(xfull(g), (uint32_t)(n_seg & 1), a.status);
-          if (got) {
-            float mf = m;
-#pragma unroll
-            for (int w = 0; w < WPH - 1; ++w) mf = fmaxf(mf, xs[w * 32 * (VPL + 2) + VPL]);
-            const float f0 = m == -INFINITY ? 0.f : exp2f(m - mf);
-            l *= f0;
-#pragma unroll
-            for (int y = 0; y < VPL; ++y) acc[y] *= f0;
-#pragma unroll
-            for (int w = 0; w < WPH - 1; ++w) {
-              const float* o = xs + w * 32 * (VPL + 2);
-              const float f = o[VPL] == -INFINITY ? 0.f : exp2f(o[VPL] - mf);
-              if (f != 0.f) {
-                l = fmaf(o[VPL + 1], f, l);
-#pragma unroll
-                for (int y = 0; y < VPL; ++y) acc[y] = fmaf(o[y], f, acc[y]);
-              }
-            }
-            m = mf;
-          }
-          if (!__all_sync(0xffffffffu, got)) ok = false;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(xempty(g));
+        for (int y = 0; y < VD / 16; ++y) {
+          if ((y & 3) != pr4) continue;  // the quad's lanes hold the same
+          mine[y * 16 + quad] = acc[y][0] + acc[y][1];
+          mine[y * 16 + 8 + quad] = acc[y][2] + acc[y][3];
         }
+        if (lane == 0) {
+          mine[VD] = ok ? m : -INFINITY;  // a part that lacks tiles counts as empty
+          mine[VD + 1] = ok ? l : 0.f;
+        }
+        __syncwarp();
+        if (par > 0 && lane == 0) mbar_arrive(xfull(g));
+      }
+      float o_sum[VPL];
+      if (par == 0) {
+        const bool got = WPH == 1 || mbar_wait(xfull(g), (uint32_t)(n_seg & 1), a.status);
+        float mf = m;
+        l = 0.f;
+#pragma unroll
+        for (int y = 0; y < VPL; ++y) o_sum[y] = 0.f;
+        if (got) {
+#pragma unroll
+          for (int w = 0; w < WPH; ++w) mf = fmaxf(mf, xs[w * (VD + 4) + VD]);
+#pragma unroll
+          for (int w = 0; w < WPH; ++w) {
+            const float* o = xs + w * (VD + 4);
+            const float f = o[VD] == -INFINITY ? 0.f : exp2f(o[VD] - mf);
+            if (f != 0.f) {
+              l = fmaf(o[VD + 1], f, l);
+#pragma unroll
+              for (int y = 0; y < VPL; ++y) o_sum[y] = fmaf(o[lane * VPL + y], f, o_sum[y]);
+            }
+          }
+          m = mf;
+        }
+        if (!__all_sync(0xffffffffu, got)) ok = false;
+        __syncwarp();
+        if (WPH > 1 && lane == 0) mbar_arrive(xempty(g));
       }
       if (par == 0) {
         if (!ok) {  // given up on a wait (reported): an empty part
           m = -INFINITY;
           l = 0.f;
 #pragma unroll
-          for (int y = 0; y < VPL; ++y) acc[y] = 0.f;
+          for (int y = 0; y < VPL; ++y) o_sum[y] = 0.f;
         }
         if (ta == 0 && tb == c.n_tiles) {
           float mf = m, lt = l, f = 1.f;
@@ -336,14 +431,14 @@ __global__ void __launch_bounds__(288, 1)
 #pragma unroll
           for (int y = 0; y < VPL; y += 2)
             *reinterpret_cast<__nv_bfloat162*>(o + y) =
-                __floats2bfloat162_rn(acc[y] * inv, acc[y + 1] * inv);
+                __floats2bfloat162_rn(o_sum[y] * inv, o_sum[y + 1] * inv);
           if (lane == 0 && a.lse)
             a.lse[(long)c.r.t0 * a.HQ + h] = lt == 0.f ? -INFINITY : (mf + log2f(lt)) * kLn2;
         } else {
           const int slot = ta == 0 ? 1 : 0;
           float* po = parts.o(cta, slot, VD) + g * VD + lane * VPL;
 #pragma unroll
-          for (int y = 0; y < VPL; ++y) po[y] = acc[y];
+          for (int y = 0; y < VPL; ++y) po[y] = o_sum[y];
           if (lane == 0) {
             float* pm = parts.ml(cta, slot, VD) + g * 2;
             pm[0] = m;
@@ -376,8 +471,7 @@ int launch(const AttnArgs& a, const Parts& parts, const UnitFlags& flags, cudaSt
     return WALL_ERR_CUDA;
   const int oR = (dl.G * (KD / 64) + VD / 64) * kBox;
   dl.stage_bytes = (oR + dl.G * KD * 4 + 1023) & ~1023;
-  const int tail = dl.G * WPH * KD * 4 + dl.G * (WPH - 1) * 32 * (VD / 32 + 2) * 4 +
-                   (2 * kMaxStages + 2 * dl.G) * 8;
+  const int tail = dl.G * WPH * (kQBytes + (VD + 4) * 4) + (2 * kMaxStages + 2 * dl.G) * 8;
   dl.stages = (226 * 1024 - 1024 - tail) / dl.stage_bytes;
   if (dl.stages > kMaxStages) dl.stages = kMaxStages;
   dl.stages -= dl.stages % WPH;
