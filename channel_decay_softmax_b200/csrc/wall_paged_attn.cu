@@ -310,11 +310,11 @@ __global__ void __launch_bounds__(kGenThreads, 3) flagged_kernel(AttnArgs a, Uni
 // Joining the units that more than one CTA worked on: o = sum of the parts
 // weighted by 2^(m_part - m), over the sum of their l, in the order of the
 // CTAs (the same bits every time).  One warp a row; 4 channels a lane.
-// One launch joins all of a call's parts, of the two kernels that it may run.
+// One launch joins all of a call's parts, of the kernels that it may run.
 constexpr int kJoinThreads = 256, kJoinY = 4;
 struct JoinSet {
   Parts parts;
-  int group;  // > 0: a part's rows are the heads of one kv head, of a single token
+  int group;  // > 0: a part's rows are tokens of `group` heads of one kv head
 };
 struct JoinSets {
   JoinSet s[2];
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(AttnArgs a, JoinS
     }
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-    if (group > 0) write_row<T, 4>(a, d.t0, d.h * group + row, lane, m, l, acc);
+    if (group > 0) write_row<T, 4>(a, d.t0 + row / group, d.h * group + row % group, lane, m, l, acc);
     else write_row<T, 4>(a, d.t0 + row, d.h, lane, m, l, acc);
   }
 }
@@ -402,7 +402,7 @@ int join(const AttnArgs& a, const JoinSets& sets, cudaStream_t stream) {
   for (int i = 0; i < sets.n; ++i) {
     const JoinSet& s = sets.s[i];
     ctas += s.parts.n_cta;
-    rows = std::max(rows, s.group > 0 ? s.group : s.parts.rows);
+    rows = std::max(rows, s.parts.rows);
   }
   return launch_behind(join_kernel<T>, dim3(ctas, std::min(kJoinY, ceil_div(rows, kJoinThreads / 32))),
                        kJoinThreads, 0, stream, a, sets);
@@ -440,28 +440,36 @@ int run_flagged(const AttnArgs& a, const UnitFlags& flags, cudaStream_t stream) 
 }
 
 // Which kernels a call runs: single-token rows stream through the decode
-// kernel and rows of requests of more through the tensor cores where those
-// cover the shape; the general kernel takes what is left.
+// kernel and rows of requests of more through the tensor cores where these
+// kernels cover the shape; the general kernel takes what is left.  A call whose
+// requests all have at most kShortRows rows (drafts) needs the decode kernel
+// alone, in a form for that many: 16 requests of 2 to 8 rows take 78 us so, 111
+// as units of 128 rows.  Beside longer requests the few rows stay with those: a
+// further launch costs each such call 5 us, and single tokens through the form
+// for many rows 57 us where their own takes 39.
 struct Route {
-  bool decode;    // the decode kernel, for requests of one row
-  bool chunk;     // the tensor-core kernel, for requests of two or more
+  bool decode;    // the decode kernel, for requests of fewer than n_min rows
+  bool chunk;     // the tensor-core kernel, for requests of n_min or more
+  int n_min;
   bool general;   // the general kernel
   Pick rows;      // the requests it takes
 };
 Route route_of(int dtype, int max_new, int H, int HQ, int K, int V) {
   Route r;
   r.decode = decode_rows_supported(dtype, H, HQ, K, V);
-  r.chunk = max_new > 1 && chunk_rows_supported(dtype, K, V);
-  r.rows.n_min = r.decode ? 2 : 1;
+  r.n_min = r.decode && few_rows(max_new) ? kShortRows + 1 : 2;
+  r.chunk = max_new >= r.n_min && chunk_rows_supported(dtype, K, V);
+  r.rows.n_min = r.decode ? r.n_min : 1;
   r.rows.n_max = r.chunk ? 1 : 0x7fffffff;
-  r.general = !r.decode || (max_new > 1 && !r.chunk);
+  r.general = !r.decode || (max_new >= r.n_min && !r.chunk);
   return r;
 }
 
 struct AttnWs {
   size_t dec_desc, dec_data, chunk_desc, chunk_data, qh, flags, gen_desc, gen_data, total;
 };
-AttnWs attn_ws(const Route& r, int N, int T, int H, int HQ, int K, int V) {
+int decode_part_rows(int max_new, int G) { return few_rows(max_new) ? max_new * G : G; }
+AttnWs attn_ws(const Route& r, int N, int T, int max_new, int H, int HQ, int K, int V) {
   AttnWs w;
   size_t off = 0;
   auto take = [&](bool need, int ctas, int rows, size_t& desc, size_t& data) {
@@ -470,7 +478,7 @@ AttnWs attn_ws(const Route& r, int N, int T, int H, int HQ, int K, int V) {
     data = off;
     off += need ? al256(sizeof(float) * 2 * ctas * Parts::stride_of(rows, V)) : 0;
   };
-  take(r.decode, kSms, HQ / H, w.dec_desc, w.dec_data);
+  take(r.decode, kSms, decode_part_rows(max_new, HQ / H), w.dec_desc, w.dec_data);
   take(r.chunk, kSms, kChunkRows, w.chunk_desc, w.chunk_data);
   w.qh = off;
   off += r.chunk ? al256((size_t)2 * T * HQ * K) : 0;
@@ -493,7 +501,7 @@ Parts parts_at(void* ws, size_t desc, size_t data, int rows, int ctas) {
 }  // namespace
 
 size_t paged_attn_ws(int dtype, int N, int T, int max_new, int H, int HQ, int K, int V) {
-  return attn_ws(route_of(dtype, max_new, H, HQ, K, V), N, T, H, HQ, K, V).total;
+  return attn_ws(route_of(dtype, max_new, H, HQ, K, V), N, T, max_new, H, HQ, K, V).total;
 }
 
 int paged_attn(const PagedAttnProblem& pb, void* ws, cudaStream_t stream) {
@@ -510,7 +518,8 @@ int paged_attn(const PagedAttnProblem& pb, void* ws, cudaStream_t stream) {
   a.o = pb.o; a.lse = pb.lse;
   a.status = device_status();
   const Route r = route_of(pb.dtype, pb.max_new, pb.H, pb.HQ, pb.K, pb.V);
-  const AttnWs w = attn_ws(r, pb.N, pb.T, pb.H, pb.HQ, pb.K, pb.V);
+  a.n_min = r.n_min;
+  const AttnWs w = attn_ws(r, pb.N, pb.T, pb.max_new, pb.H, pb.HQ, pb.K, pb.V);
   UnitFlags flags = {};
   if (r.chunk) {
     flags.f = reinterpret_cast<int*>(static_cast<char*>(ws) + w.flags);
@@ -520,7 +529,7 @@ int paged_attn(const PagedAttnProblem& pb, void* ws, cudaStream_t stream) {
   JoinSets sets = {};
   if (r.decode) {
     const int G = pb.HQ / pb.H;
-    const Parts p = parts_at(ws, w.dec_desc, w.dec_data, G, kSms);
+    const Parts p = parts_at(ws, w.dec_desc, w.dec_data, decode_part_rows(pb.max_new, G), kSms);
     const int rc = decode_rows(a, p, flags, stream);  // clears the flags
     if (rc) return rc;
     sets.s[sets.n++] = {p, G};

@@ -13,6 +13,7 @@ constexpr int kSms = 148;
 constexpr int kGeneralCtas = kSms * 3;
 constexpr int kGeneralRows = 32;  // query rows of a general unit, keys of a tile
 constexpr int kChunkRows = 128;   // the same of the tensor-core kernel
+constexpr int kShortRows = 8;     // rows of a request that the decode kernel can take
 
 struct AttnArgs {
   const void* q;        // [T, HQ, K]
@@ -27,6 +28,7 @@ struct AttnArgs {
   float scale_log2;     // scale * log2(e)
   int window;           // 0: none
   int max_new;
+  int n_min;            // requests of so many rows on are the chunk (or general) kernel's
   void* o;              // [T, HQ, V]
   float* lse;           // [T, HQ] or null
   int* status;
@@ -75,14 +77,16 @@ struct UnitFlags {
   }
 };
 
-// rows of requests of two or more (wall_paged_chunk_sm100.cu): Parts of
+// rows of requests of n_min or more (wall_paged_chunk_sm100.cu): Parts of
 // kChunkRows rows, kSms CTAs; qh: bf16 [T, HQ, K] of scratch
 bool chunk_rows_supported(int dtype, int K, int V);
 int chunk_rows(const AttnArgs& a, const Parts& parts, const UnitFlags& flags, void* qh,
                cudaStream_t stream);
 
-// single-token rows (wall_paged_decode.cu): Parts of HQ / H rows, kSms CTAs; it
-// also clears the flags of the call's other units
+// rows of requests of one, or of one to max_new where few_rows() says so
+// (wall_paged_decode.cu): Parts of as many rows times HQ / H, kSms CTAs; it also
+// clears the flags of the call's other units
+inline bool few_rows(int max_new) { return max_new > 1 && max_new <= kShortRows; }
 bool decode_rows_supported(int dtype, int H, int HQ, int K, int V);
 int decode_rows(const AttnArgs& a, const Parts& parts, const UnitFlags& flags, cudaStream_t stream);
 

@@ -1,6 +1,6 @@
 // wall_paged_chunk_sm100.cu -- rows of requests with two or more new tokens
 // over the paged Wall cache, on the tensor cores (tcgen05 + TMEM + TMA; bf16,
-// K == V in {64, 128}): prompts, chunks of prompts, drafts.
+// K == V in {64, 128}): prompts, chunks of prompts, long drafts.
 //
 // Math.  A unit is 128 query rows of one (request, head).  With R_I the anchor
 // of the page that holds its first row,
@@ -58,9 +58,9 @@ constexpr int kUnit = 3;                  // a unit's own cost, in tiles
 // The walk over the units as calls: it runs once a unit or less, and the code of
 // this kernel's roles has to stay within what the instruction cache holds (at
 // 122 KB of it every role ran a third slower than at 83 KB).
-__device__ __noinline__ bool start_share(const Batch& bt, int window, int heads, int cta, int n_cta,
+__device__ __noinline__ bool start_share(const Batch& bt, int window, int heads, int n_min, int cta, int n_cta,
                                          FindScratch& fs, Share& sh, long long& x0, long long& x1) {
-  if (!find_start<BM, kUnit>(bt, window, heads, {2, 0x7fffffff}, kUnit + 2, cta, n_cta, fs, sh))
+  if (!find_start<BM, kUnit>(bt, window, heads, {n_min, 0x7fffffff}, kUnit + 2, cta, n_cta, fs, sh))
     return false;
   x0 = sh.begin(cta);
   x1 = sh.begin(cta + 1);
@@ -70,8 +70,8 @@ __device__ __noinline__ void start_cursor(const Batch& bt, int window, const Fin
                                           long long x, Cursor& c) {
   c = cursor_at<BM, kUnit>(bt, window, fs.req, fs.base, x);
 }
-__device__ __noinline__ void advance(const Batch& bt, int window, int heads, Cursor& c) {
-  next_unit<BM>(bt, window, heads, {2, 0x7fffffff}, c);
+__device__ __noinline__ void advance(const Batch& bt, int window, int heads, int n_min, Cursor& c) {
+  next_unit<BM>(bt, window, heads, {n_min, 0x7fffffff}, c);
 }
 __device__ __noinline__ int ending_cta(const Share& sh, const Cursor& c, long long x) {
   return sh.last_owner<kUnit>(c, x);
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   start_next();
   Share sh;
   long long x0, x1;
-  if (!start_share(a.bt, a.window, a.HQ, cta, parts.n_cta, fs, sh, x0, x1)) {
+  if (!start_share(a.bt, a.window, a.HQ, a.n_min, cta, parts.n_cta, fs, sh, x0, x1)) {
     wait_before();
     return;
   }
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         x += run.places;
-        if (x < x1) advance(a.bt, a.window, a.HQ, c);
+        if (x < x1) advance(a.bt, a.window, a.HQ, a.n_min, c);
         if (s.cnt > 0) break;
       }
       ++seg_k;
@@ -899,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// Qh = q * 2^(p + R_{page(i)} - R_I): rows of requests of two or more, a CTA a
+// Qh = q * 2^(p + R_{page(i)} - R_I): rows of requests of n_min or more, a CTA a
 // row at a time, eight channels a thread.  An exponent past +-kAnchorRange
 // flags the row's unit.
 __global__ void __launch_bounds__(256) chunk_queries_kernel(AttnArgs a, __nv_bfloat16* qh,
@@ -915,7 +915,7 @@ __global__ void __launch_bounds__(256) chunk_queries_kernel(AttnArgs a, __nv_bfl
       else hi = mid - 1;
     }
     const Request r = request_of<BM>(a.bt, lo, a.window);
-    if (t < r.t0 || t >= r.t0 + r.n || r.n < 2 || r.dead) continue;
+    if (t < r.t0 || t >= r.t0 + r.n || r.n < a.n_min || r.dead) continue;
     const int b = (t - r.t0) / BM;
     const int slot = (r.ctx + t - r.t0) >> a.shift, slot_i = (r.ctx + b * BM) >> a.shift;
     const long trow = (long)lo * a.MP;

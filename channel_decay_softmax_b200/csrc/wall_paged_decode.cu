@@ -1,31 +1,36 @@
-// wall_paged_decode.cu -- the single-token rows of a paged batch (bf16, K and
-// V in {64, 128}, up to 8 query heads a kv head).
+// wall_paged_decode.cu -- the single-token rows of a paged batch, and the rows
+// of one whose requests have at most eight (drafts); bf16, K and V in {64, 128},
+// up to 8 query heads a kv head.
 //
-// Memory-bound: a row reads its request's key rows (per query head), value
+// Memory-bound: a request's rows read its key rows (per query head), value
 // rows (shared by the G heads of a kv head) and anchors once.  One CTA per SM
 // streams an even share of the batch's 32-key tiles of (request, kv head):
 // the last warp's lane 0 keeps a ring of TMA stages full (per tile one box of
 // 64 channels x 32 rows x G heads per 128 bytes of key row -- the pages are
 // head-major, so each head's piece is contiguous -- the value boxes and the
 // page's anchors), and the tile's G heads have WPH warps each that take
-// alternate stages with a softmax state of their own (a stage is the same
-// warp's in every round, the stages being a multiple of WPH: a wait on a
+// alternate stages with a softmax state of their own.  A stage is the same
+// warp's in every round (the stages are a multiple of WPH): a wait on a
 // barrier's parity tells a phase only from the one before, which its waiter
-// has to have seen).  The share runs across
-// requests and heads, so the ring never drains between them, and a batch of
-// any lengths loads every SM alike.
+// has to have seen.  The share runs across requests and heads, so the ring
+// never drains between them, and a batch of any lengths loads every SM alike.
 //
-// A single row gives the tensor cores nothing to reuse, but as warp-level
-// matrix products (m16n8k16: 16 keys, or 16 value channels, by 8 columns)
-// the two contractions take a quarter of the instructions of fp32 FMAs, which
-// unpack every element first and bound this kernel by issue and power (32
-// requests of up to 131072 tokens: 525 us cold, 601 us at the 1000 W limit).
-// The 8 columns hold the one vector's parts: q 2^(...) as a sum of three
-// bf16 (24 bits: nothing of the fp32 value is lost) and P as a sum of two (to
-// 2^-16, beside the output's rounding of 2^-8; its sum is taken in fp32
-// before that), so that products are exact and sums are fp32.
+// So few rows give the tensor cores little to reuse, but as warp-level matrix
+// products (m16n8k16: 16 keys, or 16 value channels, by 8 columns) the two
+// contractions take a quarter of the instructions of fp32 FMAs, which unpack
+// every element first and bound this kernel by issue and power (32 requests of
+// up to 131072 tokens: 506 us cold and 587 us at the 1000 W limit; so 450 and
+// 453, 3.1 GB at 6.9 TB/s).
+//
+// One row: the 8 columns hold the one vector's parts, q 2^(...) as a sum of
+// three bf16 (24 bits: nothing of the fp32 value is lost) and P as a sum of two
+// (to 2^-16, beside the output's rounding of 2^-8).  Up to eight rows: the
+// columns are the rows, q 2^(...) and P rounded to bf16 as the kernel for
+// longer requests rounds them (a second part of each: 91 us for the drafts
+// that take 72).  P's sum is of its fp32 values, sums are fp32.
 #include <cuda.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "sm100_ptx.cuh"
@@ -44,7 +49,7 @@ constexpr int kMaxStages = 16;
 
 // A query's operand in shared memory: per (lane & 3, part) the words of its
 // k-steps, 80 bytes apart so that a warp's vector reads meet few banks twice
-constexpr int kQGroup = 80, kQBytes = 12 * kQGroup;
+constexpr int kQGroup = 80, kQBytes = 1024;
 
 __device__ __forceinline__ void ldsm4(uint32_t (&d)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -73,13 +78,35 @@ __device__ __forceinline__ float rest_of(float x, float part) {
   return fabsf(part) == INFINITY ? 0.f : x - part;
 }
 
+// an 8 x 8 block of bf16 pairs, transposed among the lanes
+__device__ __forceinline__ uint32_t transpose8(uint32_t w) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(w));
+  return d;
+}
+// x 2^e, in two steps: 2^e itself may lie outside fp32 where the product does not
+__device__ __forceinline__ float times_pow2(float x, int e) {
+  e = min(max(e, -252), 252);
+  const int half = e >> 1;
+  return x * __int_as_float((half + 127) << 23) * __int_as_float((e - half + 127) << 23);
+}
+// any half of the word that is an infinity or a NaN
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+__device__ __forceinline__ uint32_t pair_mask(int j, int ja, int jb) {  // keys j, j + 1 in [ja, jb)
+  return (j >= ja && j < jb ? 0xffffu : 0u) | (j + 1 >= ja && j + 1 < jb ? 0xffff0000u : 0u);
+}
+
 struct DecodeLaunch {
   int G, stages, stage_bytes;
+  int rows;  // requests of up to so many rows are this kernel's
   int* clear;  // words to clear, for the kernels behind this one
   long clear_n;
 };
 
-template <int KD, int VD, int WPH>
+// kMany: requests of one to kShortRows rows, otherwise those of one
+template <int KD, int VD, int WPH, bool kMany>
 __global__ void __launch_bounds__(288, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, AttnArgs a, Parts parts,
@@ -95,15 +122,16 @@ __global__ void __launch_bounds__(288, 1)
   const int oR = oV + (VD / 64) * kBox;              // anchors int32 [G][KD]
   const int nw = G * WPH;                            // consumer warps
   uint8_t* qts = smem + stages * dl.stage_bytes;     // [nw] query operands
-  float* xch = reinterpret_cast<float*>(qts + nw * kQBytes);  // [G][WPH][VD + 4]: sums, m, l
-  uint64_t* bars = reinterpret_cast<uint64_t*>(xch + nw * (VD + 4));
+  constexpr int XW = (kMany ? kShortRows : 1) * (VD + 4);          // a warp's states: per row sums, m, l
+  float* xch = reinterpret_cast<float*>(qts + nw * kQBytes);  // [G][WPH][XW]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(xch + nw * XW);
   auto full = [&](int st) { return smem_u32(&bars[st]); };
   auto empty = [&](int st) { return smem_u32(&bars[stages + st]); };
   auto xfull = [&](int g) { return smem_u32(&bars[2 * stages + g]); };
   auto xempty = [&](int g) { return smem_u32(&bars[2 * stages + G + g]); };
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cta = blockIdx.x;
-  const Pick pk = {1, 1};
+  const Pick pk = {1, dl.rows};
   start_next();
   for (long i = (long)cta * blockDim.x + threadIdx.x; i < dl.clear_n; i += (long)gridDim.x * blockDim.x)
     dl.clear[i] = 0;
@@ -213,244 +241,439 @@ __global__ void __launch_bounds__(288, 1)
         if (x < x1) next_unit<kTile>(a.bt, a.window, a.H, pk, c);
         continue;
       }
-      const int kh = c.h, h = kh * G + g;
-      const int pos = c.r.kv - 1;  // of the row; its request's last key
-      const int lo_key = c.r.dead ? 0 : max(0, pos - win + 1);
+      const int kh = c.h, h = kh * G + g, n = c.r.n;
       const int lo_tile = tile_lo(c.r, c.b);
-      // the query and its prefix beyond the anchor of its own page
-      float qv[QPL], pv[QPL];
-      int Rq[QPL];
-      {
-        const long e = ((long)c.r.t0 * a.HQ + h) * KD + lane * QPL;
-        const int slot = pos >> a.shift;
-        const int page = !c.r.dead && slot < a.MP
-                             ? page_of(a.table, (long)c.r.i * a.MP, slot, a.NP) : -1;
-#pragma unroll
-        for (int y = 0; y < QPL; ++y) {
-          qv[y] = to_f32(q[e + y]) * a.scale_log2;
-          pv[y] = a.p[e + y];
-          Rq[y] = page >= 0 ? a.rp[((long)page * a.HQ + h) * KD + lane * QPL + y] : 0;
-        }
-      }
-      float m = -INFINITY, l = 0.f;
-      float acc[VD / 16][4];  // channels 16 c + quad (parts 0, 1) and + 8
-#pragma unroll
-      for (int y = 0; y < VD / 16; ++y)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[y][e] = 0.f;
-      int page_at = -1;
-      for (int t = ta; t < tb; ++t) {
-        const int cs = st;
-        const uint32_t cp = phase;
-        if (++st == stages) {
-          st = 0;
-          phase ^= 1;
-        }
-        if (!ok || cs % WPH != par) continue;  // another warp's stage
-        {
-          const bool got = mbar_wait(full(cs), cp, a.status);
-          if (!__all_sync(0xffffffffu, got)) {
+      // this warp's tiles of the run, one after the other
+      auto each_tile = [&](auto body) {
+        for (int t = ta; t < tb; ++t) {
+          const int cs = st;
+          const uint32_t cp = phase;
+          if (++st == stages) {
+            st = 0;
+            phase ^= 1;
+          }
+          if (!ok || cs % WPH != par) continue;  // another warp's stage
+          if (!__all_sync(0xffffffffu, mbar_wait(full(cs), cp, a.status))) {
             ok = false;
             continue;
           }
-        }
-        const uint8_t* sb = smem + cs * dl.stage_bytes;
-        const int j0 = (lo_tile + t) * kTile;
-        if ((j0 >> a.shift) != page_at) {
-          // the query against this page: scale * log2(e) * q * 2^(p + R - R_c),
-          // its three parts to the words that the fragments read
-          const int* R = reinterpret_cast<const int*>(sb + oR) + g * KD + lane * QPL;
+          body(smem + cs * dl.stage_bytes, (lo_tile + t) * kTile);
           __syncwarp();
-#pragma unroll
-          for (int y = 0; y < QPL; y += 2) {
-            float x0 = qv[y] * exp2f(pv[y] + (float)(Rq[y] - R[y]));
-            float x1 = qv[y + 1] * exp2f(pv[y + 1] + (float)(Rq[y + 1] - R[y + 1]));
-            const int ch = lane * QPL + y, pair = (ch & 15) >> 1;
-            uint8_t* w = qt + (pair & 3) * 3 * kQGroup + ((ch >> 4) * 2 + (pair >> 2)) * 4;
-#pragma unroll
-            for (int z = 0; z < 3; ++z) {
-              const uint32_t h = pack2(x0, x1);
-              *reinterpret_cast<uint32_t*>(w + z * kQGroup) = h;
-              x0 = rest_of(x0, low_of(h));
-              x1 = rest_of(x1, high_of(h));
+          if (lane == 0) mbar_arrive(empty(cs));
+        }
+      };
+      float* mine = xch + (g * WPH + par) * XW;
+      // the first of the head's warps has taken the last run's state from here
+      auto may_lay = [&] {
+        if (!__all_sync(0xffffffffu, ok)) ok = false;
+        return par == 0 || n_seg == 0 ||
+               __all_sync(0xffffffffu, mbar_wait(xempty(g), (uint32_t)((n_seg - 1) & 1), a.status));
+      };
+      bool laid;
+      int page_at = -1;
+      if constexpr (!kMany) {
+        const int pos = c.r.kv - 1;  // of the row; its request's last key
+        const int lo_key = c.r.dead ? 0 : max(0, pos - win + 1);
+        // the query and its prefix beyond the anchor of its own page
+        float qv[QPL], pv[QPL];
+        int Rq[QPL];
+        {
+          const long e = ((long)c.r.t0 * a.HQ + h) * KD + lane * QPL;
+          const int slot = pos >> a.shift;
+          const int page = !c.r.dead && slot < a.MP
+                               ? page_of(a.table, (long)c.r.i * a.MP, slot, a.NP) : -1;
+  #pragma unroll
+          for (int y = 0; y < QPL; ++y) {
+            qv[y] = to_f32(q[e + y]) * a.scale_log2;
+            pv[y] = a.p[e + y];
+            Rq[y] = page >= 0 ? a.rp[((long)page * a.HQ + h) * KD + lane * QPL + y] : 0;
+          }
+        }
+        float m = -INFINITY, l = 0.f;
+        float acc[VD / 16][4];  // channels 16 c + quad (parts 0, 1) and + 8
+  #pragma unroll
+        for (int y = 0; y < VD / 16; ++y)
+  #pragma unroll
+          for (int e = 0; e < 4; ++e) acc[y][e] = 0.f;
+        each_tile([&](const uint8_t* sb, int j0) {
+          if ((j0 >> a.shift) != page_at) {
+            // the query against this page: scale * log2(e) * q * 2^(p + R - R_c),
+            // its three parts to the words that the fragments read
+            const int* R = reinterpret_cast<const int*>(sb + oR) + g * KD + lane * QPL;
+            __syncwarp();
+  #pragma unroll
+            for (int y = 0; y < QPL; y += 2) {
+              float x0 = qv[y] * exp2f(pv[y] + (float)(Rq[y] - R[y]));
+              float x1 = qv[y + 1] * exp2f(pv[y + 1] + (float)(Rq[y + 1] - R[y + 1]));
+              const int ch = lane * QPL + y, pair = (ch & 15) >> 1;
+              uint8_t* w = qt + (pair & 3) * 3 * kQGroup + ((ch >> 4) * 2 + (pair >> 2)) * 4;
+  #pragma unroll
+              for (int z = 0; z < 3; ++z) {
+                const uint32_t h = pack2(x0, x1);
+                *reinterpret_cast<uint32_t*>(w + z * kQGroup) = h;
+                x0 = rest_of(x0, low_of(h));
+                x1 = rest_of(x1, high_of(h));
+              }
+            }
+            __syncwarp();
+  #pragma unroll
+            for (int y = 0; y < KD / 8; y += 4) {
+              const uint4 u = *reinterpret_cast<const uint4*>(qt + (pr4 * 3 + part) * kQGroup + y * 4);
+              qb[y] = u.x; qb[y + 1] = u.y; qb[y + 2] = u.z; qb[y + 3] = u.w;
+            }
+            page_at = j0 >> a.shift;
+          }
+          // scores of keys quad + 8 i: 16 keys an instruction
+          float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+          const uint32_t kb = smem_u32(sb) + g * kBox + krow;
+  #pragma unroll
+          for (int ks = 0; ks < KD / 16; ++ks) {
+            const uint32_t at = kb + (ks / 4) * G * kBox + ((((ks & 3) * 2 + kch) ^ sw) << 4);
+  #pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              uint32_t ka[4];
+              ldsm4(ka, at + y * 16 * 128);
+              mma16816(d[y], ka, qb[ks * 2], qb[ks * 2 + 1]);
             }
           }
-          __syncwarp();
-#pragma unroll
-          for (int y = 0; y < KD / 8; y += 4) {
-            const uint4 u = *reinterpret_cast<const uint4*>(qt + (pr4 * 3 + part) * kQGroup + y * 4);
-            qb[y] = u.x; qb[y + 1] = u.y; qb[y + 2] = u.z; qb[y + 3] = u.w;
+          const int ja = max(0, lo_key - j0), jb = c.r.dead ? 0 : min(kTile, pos + 1 - j0);
+          float sc[4], mt = -INFINITY;
+  #pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float lo = d[y >> 1][(y & 1) * 2 + 1];
+            sc[y] = d[y >> 1][(y & 1) * 2] + (lo + __shfl_xor_sync(0xffffffffu, lo, 1));
+            const int j = quad + 8 * y;
+            if (j < ja || j >= jb) sc[y] = -INFINITY;
+            mt = fmaxf(mt, sc[y]);
           }
-          page_at = j0 >> a.shift;
-        }
-        // scores of keys quad + 8 i: 16 keys an instruction
-        float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        const uint32_t kb = smem_u32(sb) + g * kBox + krow;
+  #pragma unroll
+          for (int o = 16; o > 2; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+          if (mt > m) {  // the same for the whole warp
+            const float alpha = exp2f(m - mt);
+            l *= alpha;
+  #pragma unroll
+            for (int y = 0; y < VD / 16; ++y)
+  #pragma unroll
+              for (int e = 0; e < 4; ++e) acc[y][e] *= alpha;
+            m = mt;
+          }
+          const float use = m == -INFINITY ? 0.f : m;
+          float p[4], ps = 0.f;
+  #pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int j = quad + 8 * y;
+            p[y] = j < ja || j >= jb ? 0.f : exp2f(sc[y] - use);
+            ps += p[y];
+          }
+  #pragma unroll
+          for (int o = 16; o > 2; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
+          l += ps;
+          // P V.  Of the keys that the row does not see the values count as 0:
+          // what those rows of the page hold (NaN included) does not enter.
+          const uint32_t vb = smem_u32(sb) + oV + vrow;
+          auto add_values = [&](auto all) {
+  #pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+              uint32_t pb[2], keep[2];
+  #pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const float e0 = __shfl_sync(0xffffffffu, p[ks * 2 + y], pr4 * 8);
+                const float e1 = __shfl_sync(0xffffffffu, p[ks * 2 + y], pr4 * 8 + 4);
+                const uint32_t h = pack2(e0, e1);
+                pb[y] = (quad & 1) == 0 ? h : pack2(e0 - low_of(h), e1 - high_of(h));
+                const int j = ks * 16 + y * 8 + pr4 * 2;
+                keep[y] = pair_mask(j, ja, jb);
+              }
+  #pragma unroll
+              for (int y = 0; y < VD / 16; ++y) {
+                uint32_t va[4];
+                ldsm4_t(va, vb + (y / 4) * kBox + ks * 16 * 128 + ((((y & 3) * 2 + vch) ^ sw) << 4));
+                if constexpr (!decltype(all)::value) {
+                  va[0] &= keep[0];
+                  va[1] &= keep[0];
+                  va[2] &= keep[1];
+                  va[3] &= keep[1];
+                }
+                mma16816(acc[y], va, pb[0], pb[1]);
+              }
+            }
+          };
+          if (ja == 0 && jb == kTile) add_values(std::true_type{});
+          else add_values(std::false_type{});
+        });
+        laid = may_lay();
+        if (laid) {
 #pragma unroll
-        for (int ks = 0; ks < KD / 16; ++ks) {
-          const uint32_t at = kb + (ks / 4) * G * kBox + ((((ks & 3) * 2 + kch) ^ sw) << 4);
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            uint32_t ka[4];
-            ldsm4(ka, at + y * 16 * 128);
-            mma16816(d[y], ka, qb[ks * 2], qb[ks * 2 + 1]);
+          for (int y = 0; y < VD / 16; ++y) {
+            if ((y & 3) != pr4) continue;  // the quad's lanes hold the same
+            mine[y * 16 + quad] = acc[y][0] + acc[y][1];
+            mine[y * 16 + 8 + quad] = acc[y][2] + acc[y][3];
+          }
+          if (lane == 0) {
+            mine[VD] = ok ? m : -INFINITY;  // a part that lacks tiles counts as empty
+            mine[VD + 1] = ok ? l : 0.f;
           }
         }
-        const int ja = max(0, lo_key - j0), jb = c.r.dead ? 0 : min(kTile, pos + 1 - j0);
-        float sc[4], mt = -INFINITY;
+      } else {
+        // Up to eight rows: the columns are rows.  Lane: fragments of row
+        // `quad`, scores and sums of rows r0, r0 + 1.
+        const int r0 = pr4 * 2, ctx = c.r.kv - n;
+        // q 2^p of row `quad`, channels 8 y + r0 and the next, and the anchors of
+        // the two pages that the rows may lie in
+        const bool real = quad < n && !c.r.dead;
+        const int slot0 = ctx >> a.shift;
+        int* Rq = reinterpret_cast<int*>(qt);
+        __syncwarp();
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const float lo = d[y >> 1][(y & 1) * 2 + 1];
-          sc[y] = d[y >> 1][(y & 1) * 2] + (lo + __shfl_xor_sync(0xffffffffu, lo, 1));
-          const int j = quad + 8 * y;
-          if (j < ja || j >= jb) sc[y] = -INFINITY;
-          mt = fmaxf(mt, sc[y]);
+        for (int z = 0; z < 2; ++z) {
+          const int page = !c.r.dead && slot0 + z < a.MP
+                               ? page_of(a.table, (long)c.r.i * a.MP, slot0 + z, a.NP) : -1;
+          for (int y = lane; y < KD; y += 32)
+            Rq[z * KD + y] = page >= 0 ? a.rp[((long)page * a.HQ + h) * KD + y] : 0;
         }
+        __syncwarp();
+        Rq += (((ctx + quad) >> a.shift) > slot0 ? KD : 0) + r0;
+        float2 xq[KD / 8];
+        {
+          const long own = ((long)(c.r.t0 + (real ? quad : 0)) * a.HQ + h) * KD + r0;
 #pragma unroll
-        for (int o = 16; o > 2; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-        if (mt > m) {  // the same for the whole warp
-          const float alpha = exp2f(m - mt);
-          l *= alpha;
-#pragma unroll
-          for (int y = 0; y < VD / 16; ++y)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[y][e] *= alpha;
-          m = mt;
+          for (int y = 0; y < KD / 8; ++y) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(q + own + y * 8);
+            const float2 p = *reinterpret_cast<const float2*>(a.p + own + y * 8);
+            xq[y] = make_float2(real ? low_of(w) * a.scale_log2 * exp2f(p.x) : 0.f,
+                                real ? high_of(w) * a.scale_log2 * exp2f(p.y) : 0.f);
+          }
         }
-        const float use = m == -INFINITY ? 0.f : m;
-        float p[4], ps = 0.f;
+        // keys [lo, hi) that the lane's two rows see
+        int lo[2], hi[2];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int j = quad + 8 * y;
-          p[y] = j < ja || j >= jb ? 0.f : exp2f(sc[y] - use);
-          ps += p[y];
+        for (int x = 0; x < 2; ++x) {
+          const bool real = r0 + x < n && !c.r.dead;
+          lo[x] = real ? max(0, ctx + r0 + x - win + 1) : 0;
+          hi[x] = real ? ctx + r0 + x + 1 : 0;
         }
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, acc[VD / 16][4];
 #pragma unroll
-        for (int o = 16; o > 2; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
-        l += ps;
-        // P V.  Of the keys that the row does not see the values count as 0:
-        // what those rows of the page hold (NaN included) does not enter.
-        const uint32_t vb = smem_u32(sb) + oV + vrow;
-        auto add_values = [&](auto all) {
+        for (int y = 0; y < VD / 16; ++y)
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {
-            uint32_t pb[2], keep[2];
+          for (int e = 0; e < 4; ++e) acc[y][e] = 0.f;  // channels 16 y + quad (rows r0, r0 + 1) and + 8
+        uint32_t qh[KD / 8];  // the rows' fragments
+        each_tile([&](const uint8_t* sb, int j0) {
+          if ((j0 >> a.shift) != page_at) {
+            page_at = j0 >> a.shift;
+            const int* R = reinterpret_cast<const int*>(sb + oR) + g * KD + r0;
+#pragma unroll
+            for (int y = 0; y < KD / 8; ++y) {
+              const int2 rc = *reinterpret_cast<const int2*>(R + y * 8);
+              const int2 ro = *reinterpret_cast<const int2*>(Rq + y * 8);
+              const float x0 = times_pow2(xq[y].x, ro.x - rc.x), x1 = times_pow2(xq[y].y, ro.y - rc.y);
+              qh[y] = pack2(x0, x1);
+            }
+          }
+          // scores of keys quad + 8 i
+          float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+          const uint32_t kb = smem_u32(sb) + g * kBox + krow;
+#pragma unroll
+          for (int ks = 0; ks < KD / 16; ++ks) {
+            const uint32_t at = kb + (ks / 4) * G * kBox + ((((ks & 3) * 2 + kch) ^ sw) << 4);
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const float e0 = __shfl_sync(0xffffffffu, p[ks * 2 + y], pr4 * 8);
-              const float e1 = __shfl_sync(0xffffffffu, p[ks * 2 + y], pr4 * 8 + 4);
-              const uint32_t h = pack2(e0, e1);
-              pb[y] = (quad & 1) == 0 ? h : pack2(e0 - low_of(h), e1 - high_of(h));
-              const int j = ks * 16 + y * 8 + pr4 * 2;
-              keep[y] = (j >= ja && j < jb ? 0xffffu : 0u) | (j + 1 >= ja && j + 1 < jb ? 0xffff0000u : 0u);
+              uint32_t ka[4];
+              ldsm4(ka, at + y * 16 * 128);
+              mma16816(d[y], ka, qh[ks * 2], qh[ks * 2 + 1]);
             }
+          }
+          float mt[2] = {m[0], m[1]};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int j = j0 + quad + 8 * i;
+              float& v = d[i >> 1][(i & 1) * 2 + x];
+              if (j < lo[x] || j >= hi[x]) v = -INFINITY;
+              mt[x] = fmaxf(mt[x], v);
+            }
+#pragma unroll
+          for (int o = 16; o > 2; o >>= 1)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) mt[x] = fmaxf(mt[x], __shfl_xor_sync(0xffffffffu, mt[x], o));
+          if (__any_sync(0xffffffffu, mt[0] > m[0] || mt[1] > m[1])) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float alpha = mt[x] > m[x] ? exp2f(m[x] - mt[x]) : 1.f;
+              l[x] *= alpha;
+#pragma unroll
+              for (int y = 0; y < VD / 16; ++y) {
+                acc[y][x] *= alpha;
+                acc[y][2 + x] *= alpha;
+              }
+              m[x] = mt[x];
+            }
+          }
+          uint32_t ph[4];  // P's fragments of keys 8 i on
+          float ps[2] = {0.f, 0.f};
+          const float use[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float p[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int j = j0 + quad + 8 * i;
+              p[x] = j < lo[x] || j >= hi[x] ? 0.f : exp2f(d[i >> 1][(i & 1) * 2 + x] - use[x]);
+              ps[x] += p[x];
+            }
+            ph[i] = transpose8(pack2(p[0], p[1]));
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int o = 16; o > 2; o >>= 1) ps[x] += __shfl_xor_sync(0xffffffffu, ps[x], o);
+            l[x] += ps[x];
+          }
+          // P V.  A value row counts as 0 where no row sees its key.  One that
+          // some rows see and others do not must be finite for these products
+          // (0 * inf); where one is not, the rows go one by one.
+          const uint32_t vb = smem_u32(sb) + oV + vrow;
+          auto value = [&](uint32_t (&va)[4], int ks, int y, int ja, int jb) {
+            ldsm4_t(va, vb + (y / 4) * kBox + ks * 16 * 128 + ((((y & 3) * 2 + vch) ^ sw) << 4));
+            const uint32_t k0 = pair_mask(ks * 16 + r0, ja, jb), k1 = pair_mask(ks * 16 + 8 + r0, ja, jb);
+            va[0] &= k0;
+            va[1] &= k0;
+            va[2] &= k1;
+            va[3] &= k1;
+          };
+          auto seen_from = [&](int row) { return c.r.dead ? kTile : max(0, max(0, ctx + row - win + 1) - j0); };
+          auto seen_to = [&](int row) { return c.r.dead ? 0 : min(kTile, ctx + row + 1 - j0); };
+          const int ja = seen_from(0), jb = seen_to(n - 1);  // by some row
+          const bool part = seen_from(n - 1) > 0 || seen_to(0) < kTile;
+          bool split = false;
+          if (part) {
+            uint32_t bad = 0;
+#pragma unroll 1
+            for (int ks = 0; ks < 2; ++ks)
+#pragma unroll 4
+              for (int y = 0; y < VD / 16; ++y) {
+                uint32_t va[4];
+                value(va, ks, y, ja, jb);
+                bad |= not_finite(va[0]) | not_finite(va[1]) | not_finite(va[2]) | not_finite(va[3]);
+              }
+            split = __any_sync(0xffffffffu, bad != 0);
+          }
+          if (!part) {
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+              for (int y = 0; y < VD / 16; ++y) {
+                uint32_t va[4];
+                ldsm4_t(va, vb + (y / 4) * kBox + ks * 16 * 128 + ((((y & 3) * 2 + vch) ^ sw) << 4));
+                mma16816(acc[y], va, ph[ks * 2], ph[ks * 2 + 1]);
+              }
+          } else {
+#pragma unroll 1
+            for (int row = 0; row < (split ? n : 1); ++row) {
+              const int from = split ? seen_from(row) : ja, to = split ? seen_to(row) : jb;
+              const bool take0 = !split || row == r0, take1 = !split || row == r0 + 1;
+#pragma unroll
+              for (int y = 0; y < VD / 16; ++y) {
+                float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                  uint32_t va[4];
+                  value(va, ks, y, from, to);
+                  mma16816(t, va, ph[ks * 2], ph[ks * 2 + 1]);
+                }
+                acc[y][0] += take0 ? t[0] : 0.f;
+                acc[y][1] += take1 ? t[1] : 0.f;
+                acc[y][2] += take0 ? t[2] : 0.f;
+                acc[y][3] += take1 ? t[3] : 0.f;
+              }
+            }
+          }
+        });
+        laid = may_lay();
+        if (laid) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float* row = mine + (r0 + x) * (VD + 4);
+            if (r0 + x >= n) continue;
 #pragma unroll
             for (int y = 0; y < VD / 16; ++y) {
-              uint32_t va[4];
-              ldsm4_t(va, vb + (y / 4) * kBox + ks * 16 * 128 + ((((y & 3) * 2 + vch) ^ sw) << 4));
-              if constexpr (!decltype(all)::value) {
-                va[0] &= keep[0];
-                va[1] &= keep[0];
-                va[2] &= keep[1];
-                va[3] &= keep[1];
-              }
-              mma16816(acc[y], va, pb[0], pb[1]);
+              row[y * 16 + quad] = acc[y][x];
+              row[y * 16 + 8 + quad] = acc[y][2 + x];
+            }
+            if (quad == 0) {
+              row[VD] = ok ? m[x] : -INFINITY;
+              row[VD + 1] = ok ? l[x] : 0.f;
             }
           }
-        };
-        if (ja == 0 && jb == kTile) add_values(std::true_type{});
-        else add_values(std::false_type{});
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty(cs));
-      }
-      // The head's warps meet: each lays its state into shared memory in the
-      // channels' order, and the first joins them.
-      if (!__all_sync(0xffffffffu, ok)) ok = false;
-      float* xs = xch + g * WPH * (VD + 4);
-      if (par > 0 && n_seg > 0 && !__all_sync(0xffffffffu, mbar_wait(xempty(g), (uint32_t)((n_seg - 1) & 1),
-                                                                     a.status)))
-        ok = false;  // (its state is not laid down, nor announced)
-      else {
-        float* mine = xs + par * (VD + 4);
-#pragma unroll
-        for (int y = 0; y < VD / 16; ++y) {
-          if ((y & 3) != pr4) continue;  // the quad's lanes hold the same
-          mine[y * 16 + quad] = acc[y][0] + acc[y][1];
-          mine[y * 16 + 8 + quad] = acc[y][2] + acc[y][3];
         }
-        if (lane == 0) {
-          mine[VD] = ok ? m : -INFINITY;  // a part that lacks tiles counts as empty
-          mine[VD + 1] = ok ? l : 0.f;
-        }
-        __syncwarp();
-        if (par > 0 && lane == 0) mbar_arrive(xfull(g));
       }
-      float o_sum[VPL];
+      // The head's warps meet: each has laid its state into shared memory in
+      // the channels' order (one that gave up on a wait has not, nor tells of
+      // it), and the first joins them.
+      __syncwarp();
+      if (!laid) ok = false;
+      else if (par > 0 && lane == 0) mbar_arrive(xfull(g));
       if (par == 0) {
-        const bool got = WPH == 1 || mbar_wait(xfull(g), (uint32_t)(n_seg & 1), a.status);
-        float mf = m;
-        l = 0.f;
-#pragma unroll
-        for (int y = 0; y < VPL; ++y) o_sum[y] = 0.f;
-        if (got) {
-#pragma unroll
-          for (int w = 0; w < WPH; ++w) mf = fmaxf(mf, xs[w * (VD + 4) + VD]);
-#pragma unroll
-          for (int w = 0; w < WPH; ++w) {
-            const float* o = xs + w * (VD + 4);
-            const float f = o[VD] == -INFINITY ? 0.f : exp2f(o[VD] - mf);
-            if (f != 0.f) {
-              l = fmaf(o[VD + 1], f, l);
-#pragma unroll
-              for (int y = 0; y < VPL; ++y) o_sum[y] = fmaf(o[lane * VPL + y], f, o_sum[y]);
-            }
-          }
-          m = mf;
-        }
-        if (!__all_sync(0xffffffffu, got)) ok = false;
-        __syncwarp();
-        if (WPH > 1 && lane == 0) mbar_arrive(xempty(g));
-      }
-      if (par == 0) {
-        if (!ok) {  // given up on a wait (reported): an empty part
-          m = -INFINITY;
-          l = 0.f;
+        if (WPH > 1 && !__all_sync(0xffffffffu, mbar_wait(xfull(g), (uint32_t)(n_seg & 1), a.status)))
+          ok = false;
+        const bool whole = ta == 0 && tb == c.n_tiles;
+        const int slot = ta == 0 ? 1 : 0;
+        for (int row = 0; row < n; ++row) {
+          float m = -INFINITY, l = 0.f, o_sum[VPL];
 #pragma unroll
           for (int y = 0; y < VPL; ++y) o_sum[y] = 0.f;
-        }
-        if (ta == 0 && tb == c.n_tiles) {
-          float mf = m, lt = l, f = 1.f;
-          if (a.sink) {
-            const float sk = a.sink[h] * kLog2e;
-            mf = fmaxf(m, sk);
-            f = m == -INFINITY ? 0.f : exp2f(m - mf);
-            lt = l * f + exp2f(sk - mf);
+          if (ok) {  // otherwise (reported): an empty part
+            const float* xs = mine + row * (VD + 4);
+#pragma unroll
+            for (int w = 0; w < WPH; ++w) m = fmaxf(m, xs[w * XW + VD]);
+#pragma unroll
+            for (int w = 0; w < WPH; ++w) {
+              const float* o = xs + w * XW;
+              const float f = o[VD] == -INFINITY ? 0.f : exp2f(o[VD] - m);
+              if (f != 0.f) {
+                l = fmaf(o[VD + 1], f, l);
+#pragma unroll
+                for (int y = 0; y < VPL; ++y) o_sum[y] = fmaf(o[lane * VPL + y], f, o_sum[y]);
+              }
+            }
           }
-          const float inv = lt > 0.f || lt != lt ? f / lt : 0.f;
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + ((long)c.r.t0 * a.HQ + h) * VD + lane * VPL;
+          if (whole) {
+            float mf = m, lt = l, f = 1.f;
+            if (a.sink) {
+              const float sk = a.sink[h] * kLog2e;
+              mf = fmaxf(m, sk);
+              f = m == -INFINITY ? 0.f : exp2f(m - mf);
+              lt = l * f + exp2f(sk - mf);
+            }
+            const float inv = lt > 0.f || lt != lt ? f / lt : 0.f;
+            const long at = (long)(c.r.t0 + row) * a.HQ + h;
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + at * VD + lane * VPL;
 #pragma unroll
-          for (int y = 0; y < VPL; y += 2)
-            *reinterpret_cast<__nv_bfloat162*>(o + y) =
-                __floats2bfloat162_rn(o_sum[y] * inv, o_sum[y + 1] * inv);
-          if (lane == 0 && a.lse)
-            a.lse[(long)c.r.t0 * a.HQ + h] = lt == 0.f ? -INFINITY : (mf + log2f(lt)) * kLn2;
-        } else {
-          const int slot = ta == 0 ? 1 : 0;
-          float* po = parts.o(cta, slot, VD) + g * VD + lane * VPL;
+            for (int y = 0; y < VPL; y += 2)
+              *reinterpret_cast<__nv_bfloat162*>(o + y) =
+                  __floats2bfloat162_rn(o_sum[y] * inv, o_sum[y + 1] * inv);
+            if (lane == 0 && a.lse) a.lse[at] = lt == 0.f ? -INFINITY : (mf + log2f(lt)) * kLn2;
+          } else {
+            const int at = row * G + g;
+            float* po = parts.o(cta, slot, VD) + at * VD + lane * VPL;
 #pragma unroll
-          for (int y = 0; y < VPL; ++y) po[y] = o_sum[y];
-          if (lane == 0) {
-            float* pm = parts.ml(cta, slot, VD) + g * 2;
-            pm[0] = m;
-            pm[1] = l;
-            if (slot == 1 && g == 0) {
-              PartDesc d;
-              d.t0 = c.r.t0; d.rows = G; d.h = kh;
-              d.last_cta = sh.last_owner<kUnit>(c, x);
-              parts.desc[cta] = d;
+            for (int y = 0; y < VPL; ++y) po[y] = o_sum[y];
+            if (lane == 0) {
+              float* pm = parts.ml(cta, slot, VD) + at * 2;
+              pm[0] = m;
+              pm[1] = l;
             }
           }
         }
+        if (!whole && slot == 1 && g == 0 && lane == 0) {
+          PartDesc d;
+          d.t0 = c.r.t0; d.rows = G * n; d.h = kh;
+          d.last_cta = sh.last_owner<kUnit>(c, x);
+          parts.desc[cta] = d;
+        }
+        __syncwarp();
+        if (WPH > 1 && lane == 0) mbar_arrive(xempty(g));
       }
       ++n_seg;
       x += run.places;
@@ -459,10 +682,11 @@ __global__ void __launch_bounds__(288, 1)
   }
 }
 
-template <int KD, int VD, int WPH>
+template <int KD, int VD, int WPH, bool kMany>
 int launch(const AttnArgs& a, const Parts& parts, const UnitFlags& flags, cudaStream_t stream) {
   DecodeLaunch dl;
   dl.G = a.HQ / a.H;
+  dl.rows = kMany ? a.max_new : 1;
   dl.clear = flags.f;
   dl.clear_n = flags.total;
   CUtensorMap tk, tv;
@@ -471,27 +695,35 @@ int launch(const AttnArgs& a, const Parts& parts, const UnitFlags& flags, cudaSt
     return WALL_ERR_CUDA;
   const int oR = (dl.G * (KD / 64) + VD / 64) * kBox;
   dl.stage_bytes = (oR + dl.G * KD * 4 + 1023) & ~1023;
-  const int tail = dl.G * WPH * (kQBytes + (VD + 4) * 4) + (2 * kMaxStages + 2 * dl.G) * 8;
+  const int tail = dl.G * WPH * (kQBytes + (kMany ? kShortRows : 1) * (VD + 4) * 4) +
+                   (2 * kMaxStages + 2 * dl.G) * 8;
   dl.stages = (226 * 1024 - 1024 - tail) / dl.stage_bytes;
   if (dl.stages > kMaxStages) dl.stages = kMaxStages;
   dl.stages -= dl.stages % WPH;
   const int smem = dl.stages * dl.stage_bytes + tail + 1024;
+  const int threads = 32 * (dl.G * WPH + 1);
   static bool attr[kMaxDevices] = {};
-  if (!set_max_smem_once(paged_decode_kernel<KD, VD, WPH>, 226 * 1024, attr)) return WALL_ERR_CUDA;
-  paged_decode_kernel<KD, VD, WPH><<<parts.n_cta, 32 * (dl.G * WPH + 1), smem, stream>>>(
-      tk, tv, a, parts, dl);
+  auto* kernel = paged_decode_kernel<KD, VD, WPH, kMany>;
+  if (!set_max_smem_once(kernel, 226 * 1024, attr)) return WALL_ERR_CUDA;
+  kernel<<<parts.n_cta, threads, smem, stream>>>(tk, tv, a, parts, dl);
   return cudaGetLastError() == cudaSuccess ? WALL_OK : WALL_ERR_CUDA;
 }
 
-template <int KD, int VD>
+template <int KD, int VD, bool kMany>
 int launch_heads(const AttnArgs& a, const Parts& parts, const UnitFlags& flags, cudaStream_t stream) {
-  // eight consumer warps where the head count lets them: fewer cannot keep up
-  // with the copies
+  // warps a head: enough to keep up with the copies
   const int G = a.HQ / a.H;
-  if (G == 1) return launch<KD, VD, 8>(a, parts, flags, stream);
-  if (G == 2) return launch<KD, VD, 4>(a, parts, flags, stream);
-  if (G <= 4) return launch<KD, VD, 2>(a, parts, flags, stream);
-  return launch<KD, VD, 1>(a, parts, flags, stream);
+  if (G == 1) return launch<KD, VD, 4, kMany>(a, parts, flags, stream);
+  if (G <= 4) return launch<KD, VD, 2, kMany>(a, parts, flags, stream);
+  return launch<KD, VD, 1, kMany>(a, parts, flags, stream);
+}
+
+template <bool kMany>
+int rows_of(const AttnArgs& a, const Parts& parts, const UnitFlags& flags, cudaStream_t stream) {
+  if (a.K == 128 && a.V == 128) return launch_heads<128, 128, kMany>(a, parts, flags, stream);
+  if (a.K == 128) return launch_heads<128, 64, kMany>(a, parts, flags, stream);
+  if (a.V == 128) return launch_heads<64, 128, kMany>(a, parts, flags, stream);
+  return launch_heads<64, 64, kMany>(a, parts, flags, stream);
 }
 
 }  // namespace
@@ -503,10 +735,7 @@ bool decode_rows_supported(int dtype, int H, int HQ, int K, int V) {
 }
 
 int decode_rows(const AttnArgs& a, const Parts& parts, const UnitFlags& flags, cudaStream_t stream) {
-  if (a.K == 128 && a.V == 128) return launch_heads<128, 128>(a, parts, flags, stream);
-  if (a.K == 128) return launch_heads<128, 64>(a, parts, flags, stream);
-  if (a.V == 128) return launch_heads<64, 128>(a, parts, flags, stream);
-  return launch_heads<64, 64>(a, parts, flags, stream);
+  return few_rows(a.max_new) ? rows_of<true>(a, parts, flags, stream) : rows_of<false>(a, parts, flags, stream);
 }
 
 }  // namespace paged

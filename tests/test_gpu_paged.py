@@ -387,6 +387,46 @@ def test_attn_decode(HQ, H, K, V, dt, PS):
                sink=PS == 64, poison=True)
 
 
+@pytest.mark.parametrize("HQ,H,K,V,dt", SHAPES + [(5, 1, 128, 128, BF), (1, 1, 64, 64, BF)])
+@pytest.mark.parametrize("PS,window", [(32, 0), (64, 0), (128, 0), (64, 1), (32, 5), (128, 70)])
+def test_attn_few_rows(HQ, H, K, V, dt, PS, window):
+    """At most eight tokens a request, and that many announced: rows on both
+    sides of a page's and a tile's end, windows that end between them."""
+    _attn_case(HQ, H, K, V, PS, dt, [8, 2, 1, 0, 5, 3, 8, 7, 2], [0, 31, 64, 9, 60, 127, 249, 500, 0],
+               window=window, sink=window == 5, hint=True, poison=True)
+
+
+@pytest.mark.parametrize("window", [0, 4])
+def test_attn_few_rows_masked_values_may_be_nan(window):
+    """A value that is not finite reaches the rows that see its token alone."""
+    new, ctx, HQ, H, K = [6, 8], [90, 28], 4, 2, 128
+    x, cu, kv, table, = _attn_inputs(HQ, H, K, K, 64, BF, new, ctx)
+    call = lambda: api.wall_paged_attn(x["q"], x["p"], _i32(cu), _i32(kv), _i32(table), x["k_pages"],
+                                       x["v_pages"], x["r_pages"], window_size=window, max_new=8)
+    clean = call()
+    for bad in (float("nan"), float("inf")):
+        pages = x["v_pages"].clone()
+        for i, row in ((0, 3), (1, 5)):  # the request's token `row`
+            j = ctx[i] + row
+            x["v_pages"][int(table[i, j // 64]), :, j % 64] = bad
+        o = call()
+        for i, row in ((0, 3), (1, 5)):
+            for t in range(new[i]):
+                sees = t >= row and (window == 0 or t - row < window)
+                mine = o[cu[i] + t]
+                assert not torch.isfinite(mine).any() if sees else torch.equal(mine, clean[cu[i] + t]), (i, t)
+        x["v_pages"] = pages
+    _status_ok()
+
+
+@pytest.mark.parametrize("decay", [0.0, 0.6, 2.0])
+def test_attn_few_rows_decay(decay):
+    """Gates from none to ones that forget a page within a page: prefixes of up
+    to 2.0 * 31 * 1.5 = 93 powers of two, of the 100 that a page may hold."""
+    PS = 32
+    _attn_case(4, 1, 128, 128, PS, BF, [8, 4, 2], [200, 30, 95], hint=True, decay=decay)
+
+
 @pytest.mark.parametrize("HQ,H", [(1, 1), (2, 1), (4, 1), (8, 2)])
 def test_attn_decode_keeps_its_order_of_tiles(HQ, H):
     """Requests of one tile between requests of many, over and over: warps that
