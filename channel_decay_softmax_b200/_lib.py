@@ -146,6 +146,12 @@ def _p(t):
     return t.data_ptr()
 
 
+def _ps(*tensors):
+    """_p of each of several."""
+    return [t.data_ptr() if t is not None and t.is_cuda and t.is_contiguous() else _p(t)
+            for t in tensors]
+
+
 def _stream(stream=None):
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
@@ -307,10 +313,10 @@ def _on_device(name, fn, t, *args, stream=None):
 def wall_paged_plan(new_lens, lens, block_table, free_list, free_count, n_req, max_pages,
                     num_pages, page_size, n_tokens, cu_q, kv_lens, slot_map, admitted, lens_out,
                     free_count_out, stream=None):
-    _on_device("wall_paged_plan", lib().wall_paged_plan, cu_q, _p(new_lens), _p(lens),
-               _p(block_table), _p(free_list), _p(free_count), n_req, max_pages, num_pages,
-               page_size, n_tokens, _p(cu_q), _p(kv_lens), _p(slot_map), _p(admitted),
-               _p(lens_out), _p(free_count_out), stream=stream)
+    _on_device("wall_paged_plan", lib().wall_paged_plan, cu_q,
+               *_ps(new_lens, lens, block_table, free_list, free_count), n_req, max_pages,
+               num_pages, page_size, n_tokens,
+               *_ps(cu_q, kv_lens, slot_map, admitted, lens_out, free_count_out), stream=stream)
 
 
 def wall_paged_release(finished, lens, block_table, free_list, free_count, n_req, max_pages,
@@ -329,10 +335,10 @@ def wall_paged_append(k, v, g, cu_q, kv_lens, slot_map, n_req, n_tokens, max_new
                       page_size, num_pages, k_pages, v_pages, r_pages, carry_in, carry_out, p,
                       workspace=None, stream=None):
     ws_bytes = workspace.nbytes if workspace is not None else 0
-    _on_device("wall_paged_append", lib().wall_paged_append, k_pages, _p(k), _p(v), _p(g),
-               dtype_code(k_pages.dtype), _p(cu_q), _p(kv_lens), _p(slot_map), n_req, n_tokens,
-               max_new, H, HQ, K, V, page_size, num_pages, _p(k_pages), _p(v_pages),
-               _p(r_pages), _p(carry_in), _p(carry_out), _p(p), _p(workspace), ws_bytes,
+    _on_device("wall_paged_append", lib().wall_paged_append, k_pages, *_ps(k, v, g),
+               dtype_code(k_pages.dtype), *_ps(cu_q, kv_lens, slot_map), n_req, n_tokens,
+               max_new, H, HQ, K, V, page_size, num_pages,
+               *_ps(k_pages, v_pages, r_pages, carry_in, carry_out, p, workspace), ws_bytes,
                stream=stream)
 
 
@@ -347,8 +353,8 @@ def wall_paged_attn(q, p, cu_q, kv_lens, block_table, n_req, n_tokens, max_new, 
                     window_size, o, lse, workspace, stream=None):
     """New tokens' attention over the paged cache."""
     ws_bytes = workspace.nbytes if workspace is not None else 0
-    _on_device("wall_paged_attn", lib().wall_paged_attn, k_pages, _p(q), _p(p),
-               dtype_code(k_pages.dtype), _p(cu_q), _p(kv_lens), _p(block_table), n_req,
-               n_tokens, max_new, max_pages, H, HQ, K, V, page_size, num_pages, _p(k_pages),
-               _p(v_pages), _p(r_pages), _p(sink_bias), float(scale), int(window_size), _p(o),
-               _p(lse), _p(workspace), ws_bytes, stream=stream)
+    _on_device("wall_paged_attn", lib().wall_paged_attn, k_pages, *_ps(q, p),
+               dtype_code(k_pages.dtype), *_ps(cu_q, kv_lens, block_table), n_req, n_tokens,
+               max_new, max_pages, H, HQ, K, V, page_size, num_pages,
+               *_ps(k_pages, v_pages, r_pages, sink_bias), float(scale), int(window_size),
+               *_ps(o, lse, workspace), ws_bytes, stream=stream)

@@ -544,7 +544,7 @@ def wall_paged_plan(new_lens, lens, block_table, free_list, free_count, page_siz
         _expect("lens_out", lens_out, (N,), torch.int32)
         _expect("free_count_out", free_count_out, (1,), torch.int32)
         _same_device(lens, new_lens, lens_out, free_count_out)
-    cu_q, kv_lens, admitted = lens.new_empty(3 * N + 1).split((N + 1, N, N))
+    cu_q, kv_lens, admitted = lens.new_empty(N + 1), lens.new_empty(N), lens.new_empty(N)
     slot_map = lens.new_empty(n_tokens, dtype=torch.int64)
     L.wall_paged_plan(new_lens, lens, block_table, free_list, free_count, N, MP, NP, PS, n_tokens,
                       cu_q, kv_lens, slot_map, admitted, lens_out, free_count_out)
