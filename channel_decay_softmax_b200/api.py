@@ -646,7 +646,8 @@ def wall_paged_attn(q, p, cu_q, kv_lens, block_table, k_pages, v_pages, r_pages,
 
     One token a request, several, whole prompts and mixtures of them take the
     same call.  max_new: a bound on a request's rows, when the caller knows
-    one (1 for a plain decode step, which then launches less).  A request with
+    one: 1 for a plain decode step and up to 8 for drafts have kernels of
+    their own.  A request with
     fewer cached tokens than rows (refused: 0) sees nothing: o = 0, lse = -inf
     (the sink's bias, if there is one).  Rows past cu_q[N] are left as they
     are."""

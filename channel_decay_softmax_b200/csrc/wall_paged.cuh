@@ -71,13 +71,20 @@ __device__ __forceinline__ int page_anchor(long long P) {
 }
 
 // The packed batch: request i owns rows [cu[i], cu[i+1]) of q, and keys
-// [0, kv[i]) of its pages.  Offsets are clamped into [0, T], so that a bad
-// array cannot send a kernel out of bounds.
+// [0, kv[i]) of its pages.  Offsets are clamped into [0, T] and lengths past
+// `cap` (what the block table can hold) read as 0, a refused request's, so that
+// a bad array can send a kernel neither out of bounds nor through tiles without
+// end.
 struct Batch {
   const int* cu;
   const int* kv;
   int N;
   int T;
+  int cap;
+  __device__ __forceinline__ int keys(int i) const {
+    const int n = kv[i];
+    return n > cap ? 0 : n;
+  }
   __device__ __forceinline__ int clamp_row(int r) const { return min(max(r, 0), T); }
   __device__ __forceinline__ int start(int i) const { return clamp_row(cu[i]); }
   __device__ __forceinline__ int rows(int i) const {
@@ -115,7 +122,7 @@ __device__ __forceinline__ Request request_of(const Batch& bt, int i, int window
   r.i = i;
   r.t0 = bt.start(i);
   r.n = bt.rows(i);
-  r.kv = bt.kv[i];
+  r.kv = bt.keys(i);
   r.ctx = r.kv - r.n;
   r.dead = r.kv < r.n;
   r.nb = (r.n + TB - 1) / TB;

@@ -331,7 +331,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) join_kernel(AttnArgs a, JoinS
   const int cta = blockIdx.x - (second ? sets.s[0].parts.n_cta : 0);
   if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int i = threadIdx.x; i < a.bt.N; i += kJoinThreads)
-      if (a.bt.rows(i) > a.max_new) record_status(a.status, WALL_ERR_INVALID_ARG);
+      if (a.bt.rows(i) > a.max_new || (a.bt.rows(i) > 0 && a.bt.kv[i] > a.bt.cap))
+        record_status(a.status, WALL_ERR_INVALID_ARG);
   const PartDesc d = parts.desc[cta];
   if (d.last_cta < 0) return;
   const int np = d.last_cta - cta + 1;
@@ -508,6 +509,7 @@ int paged_attn(const PagedAttnProblem& pb, void* ws, cudaStream_t stream) {
   AttnArgs a;
   a.q = pb.q; a.p = pb.p;
   a.bt.cu = pb.cu; a.bt.kv = pb.kv; a.bt.N = pb.N; a.bt.T = pb.T;
+  a.bt.cap = pb.MP << pb.shift;
   a.table = pb.table; a.MP = pb.MP; a.NP = pb.NP; a.shift = pb.shift;
   a.H = pb.H; a.HQ = pb.HQ; a.K = pb.K; a.V = pb.V;
   a.kp = pb.k_pages; a.vp = pb.v_pages; a.rp = pb.r_pages;

@@ -19,7 +19,7 @@
 // products (m16n8k16: 16 keys, or 16 value channels, by 8 columns) the two
 // contractions take a quarter of the instructions of fp32 FMAs, which unpack
 // every element first and bound this kernel by issue and power (32 requests of
-// up to 131072 tokens: 506 us cold and 587 us at the 1000 W limit; so 450 and
+// 4096 to 16000 tokens: 506 us cold and 587 us at the 1000 W limit; so 450 and
 // 453, 3.1 GB at 6.9 TB/s).
 //
 // One row: the 8 columns hold the one vector's parts, q 2^(...) as a sum of

@@ -105,9 +105,12 @@ size_t wall_paged_attn_workspace(int dtype, int n_req, int n_tokens, int max_new
  *   o = sum_j softmax(s, sink)_j v_j,   lse = log-sum-exp (natural)
  * In: q [n_tokens, HQ, K]; p of the same rows from wall_paged_append;
  * max_new a bound on a request's rows (0: none known; a request beyond it
- * records WALL_ERR_INVALID_ARG); sink_bias [HQ] fp32 or NULL.  Out:
+ * records WALL_ERR_INVALID_ARG; 1 and up to 8 have kernels of their own, for
+ * plain steps and for drafts); sink_bias [HQ] fp32 or NULL.  Out:
  * o [n_tokens, HQ, V]; lse [n_tokens, HQ] fp32 (may be NULL).  A request with
  * kv_lens < n sees nothing: o = 0, lse = -inf (the sink's bias with a sink).
+ * One with kv_lens beyond max_pages * page_size is taken for such a one, and
+ * records WALL_ERR_INVALID_ARG.
  * Rows past cu_q[n_req] are left as they are.  Table entries of pages that no
  * row sees (before the window) may be anything.
  */

@@ -593,6 +593,39 @@ def test_attn_reports_bad_pages_and_bounds():
     _status_ok()
 
 
+@pytest.mark.parametrize("HQ,H,K,dt", [(2, 1, 64, BF), (12, 1, 64, BF), (2, 1, 64, F32)])
+@pytest.mark.parametrize("new,mx", [([1, 1], 1), ([1, 5], 8), ([1, 40], None), ([40, 3], None)])
+def test_attn_lengths_past_the_table_are_refused(HQ, H, K, dt, new, mx):
+    """A length beyond what the block table holds (up to the largest int) is
+    reported, costs nothing and leaves the other requests as they are."""
+    x, cu, kv, table = _attn_inputs(HQ, H, K, K, 64, dt, new, [100, 200])
+    call = lambda lens: api.wall_paged_attn(x["q"], x["p"], _i32(cu), _i32(lens), _i32(table),
+                                            x["k_pages"], x["v_pages"], x["r_pages"], max_new=mx)
+    want = call(kv)
+    _status_ok()
+    for far in (table.shape[1] * 64 + 1, 2 ** 31 - 1):
+        o = call([kv[0], far])
+        assert L.wall_get_status() == L.WALL_ERR_INVALID_ARG
+        assert (o[cu[1]:] == 0).all()
+        assert (o[:cu[1]] - want[:cu[1]]).abs().max() <= 2e-2  # another division of the work
+
+
+@pytest.mark.parametrize("new,mx", [([1], 1), ([5], None), ([700], None)])
+def test_append_lengths_of_the_largest_int_are_refused(new, mx):
+    HQ, H, K, PS = 2, 1, 64, 64
+    pools = dict(k_pages=torch.zeros(16, HQ, PS, K, dtype=BF, device=DEV),
+                 v_pages=torch.zeros(16, H, PS, K, dtype=BF, device=DEV),
+                 r_pages=torch.zeros(16, HQ, K, dtype=torch.int32, device=DEV))
+    T = new[0]
+    one = torch.ones(T, H, K, dtype=BF, device=DEV)
+    for far in (2 ** 31 - 1, 2 ** 31 - 100):
+        carry = torch.full((1, HQ, K), 7, dtype=torch.int64, device=DEV)
+        api.wall_paged_append(one, one, torch.ones(T, HQ, K, dtype=BF, device=DEV), _i32([0, T]),
+                              _i32([far]), torch.arange(T, device=DEV), carry=carry, max_new=mx, **pools)
+        _status_ok()
+        assert (carry == 7).all() and all((t == 0).all() for t in pools.values())
+
+
 def test_attn_pages_before_the_window_may_be_gone():
     x, cu, kv, table = _attn_inputs(4, 2, 128, 128, 32, BF, [1, 130], [300, 290])
     args = lambda tb: (x["q"], x["p"], _i32(cu), _i32(kv), _i32(tb), x["k_pages"], x["v_pages"],
