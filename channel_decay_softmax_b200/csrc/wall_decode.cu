@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(32 * (kStep ? 10 : 9), 1)
   if (threadIdx.x == 0) {
     for (int st = 0; st < stages; ++st) {
       mbar_init(full(st), 1);
-      mbar_init(empty(st), G);  // the G warps (one per head) that take the tile
+      mbar_init(empty(st), nw);  // every consumer warp, its own tile or not
     }
     for (int g = 0; g < G; ++g) {
       mbar_init(xfull(g), 1);
@@ -513,11 +513,16 @@ __global__ void __launch_bounds__(32 * (kStep ? 10 : 9), 1)
       for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
       long c_last = -1;
       for (long j0 = k0; ok && j0 < k1; j0 += kDecTile, ++seq) {
-        if ((((int)(j0 - k0) / kDecTile) % WPH) != par) continue;  // the other warp's tile
         const int st = (int)(seq % stages);
         {
+          // the other warp's tiles too: a wait on a barrier's parity tells a
+          // phase only from the one before, which its waiter has to have seen
           const bool got = mbar_wait(full(st), (uint32_t)((seq / stages) & 1), status);
           if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+        }
+        if ((((int)(j0 - k0) / kDecTile) % WPH) != par) {  // the other warp's tile
+          if (lane == 0) mbar_arrive(empty(st));
+          continue;
         }
         const uint8_t* sb = smem + st * stage_bytes;
         const int c = (int)j0 / a.C;
