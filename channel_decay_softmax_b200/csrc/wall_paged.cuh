@@ -29,8 +29,9 @@ namespace paged {
 // read of it, or write that it reads.  Every CTA waits, on every path, so that
 // the end of one means the end of all before it.  A call's first kernel is
 // launched in stream order: all of them may read the call's inputs at once.
-// Captured, single-token attention of three requests takes 10.3 us so instead
-// of 12.3, 160 draft rows 111 instead of 113; uncaptured, 112 instead of 123.
+// Three single-token requests' attention takes 10.3 us so instead of 12.3, a
+// mixed step (plan, append, attention) 132.9 instead of 137.6, uncaptured 140
+// instead of 158.
 __device__ __forceinline__ void start_next() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -334,8 +335,8 @@ __device__ __forceinline__ void next_unit(const Batch& bt, int window, int heads
 
 // What the merge of a cut unit needs, written by the CTA that begins it.
 struct PartDesc {
-  int t0, rows, h;  // its first token, its rows (of one kv head: unused)
-  int last_cta;  // < 0: this CTA begins no unit that another one ends
+  int t0, rows, h;  // first token; rows (tokens, or tokens x heads of a kv head); (kv) head
+  int last_cta;     // < 0: this CTA begins no unit that another one ends
 };
 
 // A page's id, or -1 for an entry outside the pool (reported by the caller).

@@ -18,6 +18,10 @@
 //           sums, a scan over a request's runs makes them prefixes (exact in
 //           any order, being integers), and the same kernel forms each run
 //           from its own; g is read twice, the second time mostly from L2
+// Measured: 48 requests of one token 3.3 us (four dependent loads); six prompts
+// of 301 to 2500 tokens (110 MB, 16.8 us at the copy rate) 43 us, 35 of them the
+// last pass, which issue bounds (64 % of the slots: 8 values' fixed-point steps,
+// conversions and exp2 a thread and token).
 #include "wall_internal.h"
 #include "wall_paged.cuh"
 
@@ -31,7 +35,7 @@ constexpr int kOneSlab = 128;  // one token a request: a warp's channels, four a
 // Blocks of RL positions: a CTA takes 64 channels, sixteen half-warps of RL / 16
 // tokens each, four channels a lane.  (CTAs of 128 channels and 512 threads
 // keep the same threads resident in half as many CTAs, whose barriers then
-// leave the SM idle: 40.5 against 38.6 us for 8 prompts of 6000 tokens in all.)
+// leave the SM idle: 40.5 against 38.6 us for six prompts of 301 to 2500 tokens.)
 constexpr int kSlab = 64;
 constexpr int W = 16;
 

@@ -20,6 +20,13 @@
 // last ones balance to within a tile, and a few rows over a long context
 // spread over all SMs and are joined afterwards.
 //
+// Measured: an 8192-token prompt of 16 heads in 372 us, 739 TFLOP/s of its
+// visible pairs (45 % of the dense bf16 rate).  A tile takes 2600 cycles where
+// its MMAs are worth 1024 and its operands, copies and rescale hold the shared
+// memory for 1800: the thread that issues the MMAs waits for S's keys, P and V
+// in turn, and what it has issued runs out meanwhile.  Units of a few tiles
+// (windows) pay for their start and end: 69 us for 23 GFLOP.
+//
 // 12 warps (3 per SM sub-partition, 168 registers each):
 //   warp 0      walks the share's units, lays each one's figures into a ring in
 //               shared memory for the other roles, and issues all TMA copies:
@@ -53,7 +60,8 @@ constexpr int kKS = 3;                    // key stages
 constexpr int kVS = 2;                    // value stages
 constexpr float kRaiseAbove = 256.f;      // a tile's sum of P that raises the row's reference
 constexpr float kFlagAbove = 1.2676506e30f;  // 2^100: one that may not be held
-constexpr int kUnit = 3;                  // a unit's own cost, in tiles
+// A unit's own cost, in tiles (an 8192-token prompt: 398 us; 2: 404, 4: 402)
+constexpr int kUnit = 3;
 
 // The walk over the units as calls: it runs once a unit or less, and the code of
 // this kernel's roles has to stay within what the instruction cache holds (at

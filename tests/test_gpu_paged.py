@@ -419,6 +419,42 @@ def test_attn_few_rows_masked_values_may_be_nan(window):
     _status_ok()
 
 
+@pytest.mark.parametrize("sink", [False, True])
+def test_attn_few_rows_refused_and_padded(sink):
+    _attn_case(4, 2, 128, 128, 64, BF, [1, 8, 3, 5], [70, 0, 60, 2], sink=sink, refused=(1, 2),
+               extra_rows=5, hint=True)
+
+
+def test_attn_few_rows_are_repeatable_captured_and_on_two_streams():
+    """Units cut over many CTAs: the same bits from repeated calls, from two
+    streams at once and from a graph, whose lengths change under it."""
+    new, ctx = [8, 1, 5, 2], [6000, 300, 2500, 64]
+    x, cu, kv, table = _attn_inputs(4, 1, 128, 128, 64, BF, new, ctx, decay=0.002)
+    cu_t, kv_t, tb = _i32(cu), _i32(kv), _i32(table)
+    call = lambda: api.wall_paged_attn(x["q"], x["p"], cu_t, kv_t, tb, x["k_pages"], x["v_pages"],
+                                       x["r_pages"], max_new=8, return_lse=True)
+    first = call()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for st in streams:
+            with torch.cuda.stream(st):
+                got.append(call())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g in got for a, b in zip(first, g))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(first, out))
+    kv_t.copy_(_i32([n - 3 if n > 20 else n for n in kv]))
+    want = call()
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(want, out)) and not torch.equal(want[0], first[0])
+    _status_ok()
+
+
 @pytest.mark.parametrize("decay", [0.0, 0.6, 2.0])
 def test_attn_few_rows_decay(decay):
     """Gates from none to ones that forget a page within a page: prefixes of up
