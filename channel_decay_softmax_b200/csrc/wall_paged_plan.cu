@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanArgs a, int s
   int n_free = *a.free_count;
   if (threadIdx.x == 0 && (n_free < 0 || n_free > a.NP)) record_status(a.status, WALL_ERR_INVALID_ARG);
   n_free = min(max(n_free, 0), a.NP);
-  long long rows0 = 0, need0 = 0;  // of the requests before this round
+  long long rows0 = 0, need0 = 0;  // of the requests before these
   long long used = 0;
   for (int i0 = 0; i0 < a.N; i0 += kPlanThreads) {
     const int i = i0 + threadIdx.x;
