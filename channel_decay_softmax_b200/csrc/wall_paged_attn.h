@@ -70,9 +70,10 @@ struct UnitFlags {
   __device__ __forceinline__ long place(const Request& r, int b) const {
     return (long)r.t0 / kChunkRows + r.i + b;
   }
-  // unit: place * HQ + head
-  __device__ __forceinline__ void set(int unit, int HQ) const {
-    set_flag(f + unit);
+  // (64 bits: 2^20 requests of 4096 heads have more words than an int counts)
+  __device__ __forceinline__ int* at(long place, int h, int HQ) const { return f + place * HQ + h; }
+  __device__ __forceinline__ void set(long place, int h, int HQ) const {
+    set_flag(at(place, h, HQ));
     set_flag(any(HQ));
   }
 };

@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         nk2 = nk1;
         nk1 = s.kv - j0 < BN ? max(0, s.kv - j0) : -1;
       }
-      if (flag) flags.set(s.place * a.HQ + s.h, a.HQ);
+      if (flag) flags.set(s.place, s.h, a.HQ);
     }
 #pragma unroll 1
     for (int left = 2; ok && left > 0; --left) {
@@ -804,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         raise = 0.f;
         if (row_ok && !(r0 <= kRaiseAbove)) {
           if (r0 <= kFlagAbove) raise = (float)((__float_as_int(r0) >> 23) - 127);
-          else flags.set(s.place * a.HQ + s.h, a.HQ);  // NaN too
+          else flags.set(s.place, s.h, a.HQ);  // NaN too
         }
         tc_fence_before();
         __syncwarp();
@@ -881,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           tc_fence_before();
-          if (bad && row_ok) flags.set(s.place * a.HQ + h, a.HQ);
+          if (bad && row_ok) flags.set(s.place, h, a.HQ);
         }
         if (grp == 0 && row_ok) {
           if (whole) {
@@ -952,7 +952,7 @@ __global__ void __launch_bounds__(256) chunk_queries_kernel(AttnArgs a, __nv_bfl
         wide |= fabsf(pv[e]) > kAnchorRange;
         qv[e] *= exp2f(pv[e]);
       }
-      if (wide) flags.set((int)flags.place(r, b) * a.HQ + off / a.K, a.HQ);
+      if (wide) flags.set(flags.place(r, b), off / a.K, a.HQ);
       store8(qh + (long)t * a.HQ * a.K + off, qv);
     }
   }
