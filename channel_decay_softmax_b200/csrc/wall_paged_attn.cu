@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kGenThreads, 3) flagged_kernel(AttnArgs a, Uni
     const int first = ((int)blockIdx.x - at % (int)gridDim.x + (int)gridDim.x) % (int)gridDim.x;
     for (int x = first; x < items; x += gridDim.x) {
       const int b = x / a.HQ, h = x - b * a.HQ;
-      if (*flags.at(flags.place(r, b * GR / kChunkRows), h, a.HQ) == 0) continue;
+      if (!flags.has(flags.place(r, b * GR / kChunkRows), h, a.HQ, UnitFlags::kAgain)) continue;
       float m[kRowsPerWarp], l[kRowsPerWarp], acc[kRowsPerWarp][VPL];
       gen_tiles<T, VPL>(a, r, h, b * GR, tile_lo(r, b), 0, unit_tiles(r, b), gen_shared, m, l, acc);
 #pragma unroll

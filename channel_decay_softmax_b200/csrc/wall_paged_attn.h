@@ -55,12 +55,14 @@ struct Parts {
   }
 };
 
-// The tensor-core kernel's units that the general kernel computes again: a word
-// for each (128-row block, head), cleared by every call, and one more that says
-// whether any is set.  Block b of request i has place t0 / 128 + i + b, which
+// What the tensor-core kernel's units are: a word for each (128-row block, head),
+// cleared by every call, and one more that says whether any is to be computed
+// again by the general kernel.  Block b of request i has place t0 / 128 + i + b, which
 // no two share (a request of n rows starting at t0 ends before place
 // (t0 + n) / 128 + i + 1).
 struct UnitFlags {
+  static constexpr int kAgain = 1;  // the general kernel computes the unit again
+  static constexpr int kRises = 2;  // see kRise (wall_paged_chunk_sm100.cu)
   int* f;
   __host__ __device__ static long places(int N, int T) { return (long)T / kChunkRows + N; }
   __host__ __device__ static long count(int N, int T, int HQ) { return places(N, T) * HQ + 1; }
@@ -72,8 +74,14 @@ struct UnitFlags {
   }
   // (64 bits: 2^20 requests of 4096 heads have more words than an int counts)
   __device__ __forceinline__ int* at(long place, int h, int HQ) const { return f + place * HQ + h; }
+  __device__ __forceinline__ bool has(long place, int h, int HQ, int bit) const {
+    return (*reinterpret_cast<volatile int*>(at(place, h, HQ)) & bit) != 0;
+  }
+  __device__ __forceinline__ void mark(long place, int h, int HQ, int bit) const {
+    if (!has(place, h, HQ, bit)) atomicOr(at(place, h, HQ), bit);
+  }
   __device__ __forceinline__ void set(long place, int h, int HQ) const {
-    set_flag(at(place, h, HQ));
+    mark(place, h, HQ, kAgain);
     set_flag(any(HQ));
   }
 };

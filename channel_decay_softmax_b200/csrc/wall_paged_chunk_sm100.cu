@@ -9,8 +9,9 @@
 // where k_j is the cached row.  The anchors are whole numbers, so scaling the
 // key tile is exact: Qh is the only operand that is rounded (to bf16, half a
 // step of 2^-8, as a tensor-core operand has to be).  P is rounded to bf16
-// for P V; its sum is taken in fp32 before that.  A unit whose exponents pass
-// +-100 on some channel, or whose result holds a NaN (a value that is not finite
+// for P V; its sum is taken in fp32 before that.  A unit whose exponents
+// p_i + R_{page(i)} - R_I pass +-100 on some channel, or whose R_I - R_{page(j)}
+// passes +100, or whose result holds a NaN (a value that is not finite
 // reaches the rows that do not see it as 0 * inf), is flagged, and the general
 // kernel computes it again, exactly, behind this one.
 //
@@ -60,6 +61,12 @@ constexpr int kKS = 3;                    // key stages
 constexpr int kVS = 2;                    // value stages
 constexpr float kRaiseAbove = 256.f;      // a tile's sum of P that raises the row's reference
 constexpr float kFlagAbove = 1.2676506e30f;  // 2^100: one that may not be held
+// A key's factor 2^(R_I - R_page) below 2^-126 is no bf16 number.  A key row holds
+// up to 2^100 |k|, so as long as the unit's Qh have exponents of at most kRise
+// (gates <= 0 leave 1/2, an anchor's rounding), what such a factor leaves of a
+// product is below 2^(kRise + 100 - 127) |q k| and counts as 0.  In a unit whose
+// rows rise further the factor is applied in two steps instead.
+constexpr float kRise = 1.f;
 // A unit's own cost, in tiles (an 8192-token prompt: 398 us; 2: 404, 4: 402)
 constexpr int kUnit = 3;
 
@@ -225,6 +232,28 @@ __device__ __noinline__ void clear_rows(uint8_t* tile, int nk) {
     *reinterpret_cast<uint4*>(vt + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   __syncwarp();
+}
+
+// The second step of a key tile's factors 2^(R_I - R_page) below 2^kLowest, on
+// this thread's 16-byte chunk of channels: ri their R_I, rc the tile's pages'.
+constexpr int kLowest = -126;
+template <int KD>
+__device__ __noinline__ void scale_again(uint8_t* tile, const int* rc, int4 ri0, int4 ri1, int shift) {
+  constexpr int kChunks = KD / 8, kRowStep = 64 / kChunks;
+  const int tid = threadIdx.x - 64, ch = tid % kChunks;
+  uint8_t* kt = tile + (ch / 8) * (BN * 128);
+  auto factor = [](int lo, int hi) {
+    return pow2_bf16(min(lo - kLowest, 0)) | (pow2_bf16(min(hi - kLowest, 0)) << 16);
+  };
+  for (int r = tid / kChunks; r < BN; r += kRowStep) {
+    const int4* c = reinterpret_cast<const int4*>(rc + (r >> shift) * KD + ch * 8);
+    uint4* x = reinterpret_cast<uint4*>(kt + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+    const uint4 w = *x;
+    *x = make_uint4(mul_bf16x2(w.x, factor(ri0.x - c[0].x, ri0.y - c[0].y)),
+                    mul_bf16x2(w.y, factor(ri0.z - c[0].z, ri0.w - c[0].w)),
+                    mul_bf16x2(w.z, factor(ri1.x - c[1].x, ri1.y - c[1].y)),
+                    mul_bf16x2(w.w, factor(ri1.z - c[1].z, ri1.w - c[1].w)));
+  }
 }
 
 template <int KD>
@@ -575,6 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       const Segment s = segs[seg % kSegs];
       if (s.cnt == 0) break;
+      const bool rises = flags.has(s.place, s.h, a.HQ, UnitFlags::kRises);
       int ri[8];
       if (s.page_i >= 0) {
         const int4* r4 = reinterpret_cast<const int4*>(a.rp + ((long)s.page_i * a.HQ + s.h) * KD + ch * 8);
@@ -598,19 +628,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the request's last page hold what an earlier tile left: scaled along,
         // and masked)
         uint32_t f0 = 0, f1 = 0, f2 = 0, f3 = 0;
+        bool low = false;  // some factor lies below 2^-126 and is the first of two
         auto factors = [&](int z) {
           if ((z * 32 & (PS - 1)) != 0) return;
           const int4* rc = reinterpret_cast<const int4*>(
               reinterpret_cast<const int*>(smem + Lay::oR) + (st * Lay::kRows + (z * 32 >> a.shift)) * KD + ch * 8);
           const int4 u = rc[0], v = rc[1];
-          const int d[8] = {ri[0] - u.x, ri[1] - u.y, ri[2] - u.z, ri[3] - u.w,
-                            ri[4] - v.x, ri[5] - v.y, ri[6] - v.z, ri[7] - v.w};
+          int d[8] = {ri[0] - u.x, ri[1] - u.y, ri[2] - u.z, ri[3] - u.w,
+                      ri[4] - v.x, ri[5] - v.y, ri[6] - v.z, ri[7] - v.w};
           int most = d[0];
 #pragma unroll
           for (int e = 1; e < 8; ++e) most = max(most, d[e]);
           // beyond the operands' range, on a page that some row sees
           if (most > (int)kAnchorRange)
             flag |= j0 + z * 32 < min(s.kv, s.pos0 + s.ni) && j0 + z * 32 + PS > s.from;
+          if (rises) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              low |= d[e] < kLowest;
+              d[e] = max(d[e], kLowest);
+            }
+          }
           f0 = pow2_bf16(d[0]) | (pow2_bf16(d[1]) << 16);
           f1 = pow2_bf16(d[2]) | (pow2_bf16(d[3]) << 16);
           f2 = pow2_bf16(d[4]) | (pow2_bf16(d[5]) << 16);
@@ -640,6 +678,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           factors(z);
           scale(z, wa);
         }
+        if (low)
+          scale_again<KD>(smem + Lay::oK + st * Lay::kT,
+                          reinterpret_cast<const int*>(smem + Lay::oR) + st * Lay::kRows * KD,
+                          make_int4(ri[0], ri[1], ri[2], ri[3]), make_int4(ri[4], ri[5], ri[6], ri[7]),
+                          a.shift);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_KREADY + st));
@@ -909,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // Qh = q * 2^(p + R_{page(i)} - R_I): rows of requests of n_min or more, a CTA a
 // row at a time, eight channels a thread.  An exponent past +-kAnchorRange
-// flags the row's unit.
+// flags the row's unit; one above kRise marks it.
 __global__ void __launch_bounds__(256) chunk_queries_kernel(AttnArgs a, __nv_bfloat16* qh,
                                                             UnitFlags flags) {
   start_next();
@@ -946,12 +989,14 @@ __global__ void __launch_bounds__(256) chunk_queries_kernel(AttnArgs a, __nv_bfl
           pv[4 * e + 3] += (float)(u.w - w.w);
         }
       }
-      bool wide = false;
+      bool wide = false, rises = false;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         wide |= fabsf(pv[e]) > kAnchorRange;
+        rises |= pv[e] > kRise;
         qv[e] *= exp2f(pv[e]);
       }
+      if (rises) flags.mark(flags.place(r, b), off / a.K, a.HQ, UnitFlags::kRises);
       if (wide) flags.set(flags.place(r, b), off / a.K, a.HQ);
       store8(qh + (long)t * a.HQ * a.K + off, qv);
     }

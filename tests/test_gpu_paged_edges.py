@@ -53,6 +53,59 @@ def _attn(x, cu, kv, table, **kw):
                                x["v_pages"], x["r_pages"], return_lse=True, **kw)
 
 
+# ------------------------------------------------------------ gates of both signs
+
+@pytest.mark.parametrize("PS", [32, 64, 128])
+@pytest.mark.parametrize("HQ,H,K,dt", ROUTES)
+@pytest.mark.parametrize("new", [1, 8, 40])
+def test_attn_keys_seen_across_a_valley(new, HQ, H, K, dt, PS):
+    """Every eighth channel falls by 68 powers of two over the first page, by 62
+    more to the next one and rises by 68 among the rows: keys at the first page's
+    end count with up to 2^6, though the pages' anchors are 130 apart."""
+    gen = torch.Generator().manual_seed(new + PS)
+    n = PS + 40
+    t = np.arange(n)
+    valley = np.interp(t, [0, PS - 10, PS - 1, PS, n - 1], [0.0, -68.0, -68.0, -130.0, -62.0])
+    P = torch.tensor(-0.02 * t).float()[:, None, None].repeat(1, HQ, K)
+    P[:, :, ::8] = torch.tensor(valley).float()[:, None, None]
+    q, k = torch.randn(new, HQ, K, generator=gen), torch.randn(n, HQ, K, generator=gen)
+    q[:, :, ::8] *= 1 / 64 if dt == F32 else 1 / 16
+    k[PS:, :, ::8] = 0  # against the valley's floor the rows would see 2^68
+    x, cu, kv, table = _cache_of(P, q, k, new, H, K, PS, dt)
+    scale = K ** -0.5
+    want, lse_want = ref.attn(x["q"], x["p"], cu, kv, torch.tensor(table), x["k_pages"],
+                              x["v_pages"], x["r_pages"], PS, scale)
+    # the channels matter here: without them the result is another one
+    gone = x["q"].clone()
+    gone[:, :, ::8] = 0
+    other, _ = ref.attn(gone, x["p"], cu, kv, torch.tensor(table), x["k_pages"], x["v_pages"],
+                        x["r_pages"], PS, scale)
+    assert np.abs(want - other).max() > (1e-3 if dt == F32 else 0.05)
+    o, lse = _attn(x, cu, kv, table, scale=scale, max_new=new)
+    _status_ok()
+    assert_fwd(dt, o, want, lse, lse_want)
+
+
+def test_attn_long_zigzag():
+    """Channels that fall and rise by 60 powers of two every 80 tokens on a slow
+    way down, over many pages and several units of rows."""
+    HQ, H, K, PS, new, n = 2, 1, 128, 64, 300, 700
+    gen = torch.Generator().manual_seed(3)
+    t = np.arange(n)
+    zig = -0.15 * t + 60.0 * np.abs((t % 80) / 40.0 - 1.0)
+    P = torch.tensor(-0.01 * t).float()[:, None, None].repeat(1, HQ, K)
+    P[:, :, ::16] = torch.tensor(zig).float()[:, None, None]
+    q, k = torch.randn(new, HQ, K, generator=gen), torch.randn(n, HQ, K, generator=gen)
+    low = torch.tensor(zig < np.maximum.accumulate(zig[::-1])[::-1] - 4.0)
+    k[low, :, ::16] = 0   # keys that a later row would see at more than 2^4
+    x, cu, kv, table = _cache_of(P, q, k, new, H, K, PS, BF)
+    want, lse_want = ref.attn(x["q"], x["p"], cu, kv, torch.tensor(table), x["k_pages"],
+                              x["v_pages"], x["r_pages"], PS, K ** -0.5)
+    o, lse = _attn(x, cu, kv, table)
+    _status_ok()
+    assert_fwd(BF, o, want, lse, lse_want)
+
+
 # --------------------------------------------------------------- the largest batches
 
 def test_attn_flags_of_the_largest_batches():
