@@ -339,6 +339,12 @@ struct PartDesc {
   int last_cta;     // < 0: this CTA begins no unit that another one ends
 };
 
+// 2^(sink - m), in log2: a sink of -inf is none, also beside m = -inf (a row that
+// sees nothing).
+__device__ __forceinline__ float sink_weight(float sink, float m) {
+  return sink == -INFINITY ? 0.f : exp2f(sink - m);
+}
+
 // A page's id, or -1 for an entry outside the pool (reported by the caller).
 __device__ __forceinline__ int page_of(const int* table, long row, int slot, int num_pages) {
   const int id = table[row + slot];

@@ -213,7 +213,7 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, long token, int h, 
     const float sk = a.sink[h] * kLog2e;
     mf = fmaxf(m, sk);
     f = m == -INFINITY ? 0.f : exp2f(m - mf);
-    lt = l * f + exp2f(sk - mf);
+    lt = l * f + sink_weight(sk, mf);
   }
   const float inv = lt > 0.f || lt != lt ? f / lt : 0.f;  // a row that sees nothing: 0
   if (lane * VPL < a.V) {

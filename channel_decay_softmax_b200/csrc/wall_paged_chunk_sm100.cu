@@ -881,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float lt = l0 * a0 + l1 * a1;
         float inv = 1.f;
         if (whole) {
-          if (a.sink) lt += exp2f(a.sink[h] * kLog2e - m_f);
+          if (a.sink) lt += sink_weight(a.sink[h] * kLog2e, m_f);
           inv = lt > 0.f || lt != lt ? 1.f / lt : 0.f;  // a row that sees nothing: 0
         }
         const float f0 = a0 * inv, f1 = a1 * inv;

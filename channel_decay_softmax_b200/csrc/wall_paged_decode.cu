@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(288, 1)
               const float sk = a.sink[h] * kLog2e;
               mf = fmaxf(m, sk);
               f = m == -INFINITY ? 0.f : exp2f(m - mf);
-              lt = l * f + exp2f(sk - mf);
+              lt = l * f + sink_weight(sk, mf);
             }
             const float inv = lt > 0.f || lt != lt ? f / lt : 0.f;
             const long at = (long)(c.r.t0 + row) * a.HQ + h;

@@ -106,6 +106,31 @@ def test_attn_long_zigzag():
     assert_fwd(BF, o, want, lse, lse_want)
 
 
+# ------------------------------------------------------------------ infinite sinks
+
+@pytest.mark.parametrize("HQ,H,K,dt", ROUTES)
+@pytest.mark.parametrize("new,ctx,mx", [([1, 1, 1], [70, 0, 6000], 1), ([3, 8, 1], [70, 5, 6000], 8),
+                                        ([40, 20, 1, 150], [70, 0, 3, 900], None)])
+def test_attn_sink_of_minus_infinity_is_no_sink(HQ, H, K, dt, new, ctx, mx):
+    """A head whose sink is switched off: bit for bit the call without a sink,
+    the rows of refused requests (which see nothing) included."""
+    x, cu, kv, table = tp._attn_inputs(HQ, H, K, K, 64, dt, new, ctx, refused=(1,), decay=0.002)
+    o, lse = _attn(x, cu, kv, table, max_new=mx)
+    off = torch.full((HQ,), -math.inf, device=DEV)
+    o2, lse2 = _attn(x, cu, kv, table, max_new=mx, sink_bias=off)
+    _status_ok()
+    assert (o2[cu[1]:cu[2]] == 0).all() and (lse2[cu[1]:cu[2]] == -math.inf).all()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    if HQ > 1:  # one head with, the others without
+        off[0] = 0.3
+        one = torch.full((HQ,), 0.3, device=DEV)
+        o3, lse3 = _attn(x, cu, kv, table, max_new=mx, sink_bias=off)
+        o4, lse4 = _attn(x, cu, kv, table, max_new=mx, sink_bias=one)
+        assert torch.equal(o3[:, 0], o4[:, 0]) and torch.equal(lse3[:, 0], lse4[:, 0])
+        assert torch.equal(o3[:, 1:], o[:, 1:]) and torch.equal(lse3[:, 1:], lse[:, 1:])
+        _status_ok()
+
+
 # --------------------------------------------------------------- the largest batches
 
 def test_attn_flags_of_the_largest_batches():
