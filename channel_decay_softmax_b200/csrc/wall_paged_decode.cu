@@ -79,6 +79,14 @@ __device__ __forceinline__ float high_of(uint32_t w) { return __uint_as_float(w 
 __device__ __forceinline__ float rest_of(float x, float part) {
   return fabsf(part) == INFINITY ? 0.f : x - part;
 }
+// P's two bf16 parts: its leading 8 bits and the rest (to 2^-16 of it).  Neither
+// is below 0, nor 0 where P is not: an infinite value stays infinite times both.
+__device__ __forceinline__ float lead_of(float p) {
+  return __uint_as_float(__float_as_uint(p) & 0xffff0000u);
+}
+__device__ __forceinline__ float trail_of(float p) {
+  return fmaxf(p - lead_of(p), fminf(p, 1.17549435e-38f));  // 2^-126
+}
 
 // an 8 x 8 block of bf16 pairs, transposed among the lanes
 __device__ __forceinline__ uint32_t transpose8(uint32_t w) {
@@ -360,12 +368,14 @@ __global__ void __launch_bounds__(288, 1)
             m = mt;
           }
           const float use = m == -INFINITY ? 0.f : m;
-          float p[4], ps = 0.f;
+          uint32_t pw[4];  // a key's P: first part and second
+          float ps = 0.f;
   #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const int j = quad + 8 * y;
-            p[y] = j < ja || j >= jb ? 0.f : exp2f(sc[y] - use);
-            ps += p[y];
+            const float p = j < ja || j >= jb ? 0.f : exp2f(sc[y] - use);
+            ps += p;
+            pw[y] = pack2(lead_of(p), trail_of(p));
           }
   #pragma unroll
           for (int o = 16; o > 2; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
@@ -379,10 +389,9 @@ __global__ void __launch_bounds__(288, 1)
               uint32_t pb[2], keep[2];
   #pragma unroll
               for (int y = 0; y < 2; ++y) {
-                const float e0 = __shfl_sync(0xffffffffu, p[ks * 2 + y], pr4 * 8);
-                const float e1 = __shfl_sync(0xffffffffu, p[ks * 2 + y], pr4 * 8 + 4);
-                const uint32_t h = pack2(e0, e1);
-                pb[y] = (quad & 1) == 0 ? h : pack2(e0 - low_of(h), e1 - high_of(h));
+                const uint32_t w0 = __shfl_sync(0xffffffffu, pw[ks * 2 + y], pr4 * 8);
+                const uint32_t w1 = __shfl_sync(0xffffffffu, pw[ks * 2 + y], pr4 * 8 + 4);
+                pb[y] = __byte_perm(w0, w1, (quad & 1) == 0 ? 0x5410 : 0x7632);
                 const int j = ks * 16 + y * 8 + pr4 * 2;
                 keep[y] = pair_mask(j, ja, jb);
               }
@@ -524,9 +533,8 @@ __global__ void __launch_bounds__(288, 1)
               p[x] = j < lo[x] || j >= hi[x] ? 0.f : exp2f(d[i >> 1][(i & 1) * 2 + x] - use[x]);
               ps[x] += p[x];
             }
-            const uint32_t w = pack2(p[0], p[1]);
-            ph[i] = transpose8(w);
-            pl[i] = transpose8(pack2(p[0] - low_of(w), p[1] - high_of(w)));
+            ph[i] = transpose8(__byte_perm(__float_as_uint(p[0]), __float_as_uint(p[1]), 0x7632));
+            pl[i] = transpose8(pack2(trail_of(p[0]), trail_of(p[1])));
           }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {

@@ -131,6 +131,54 @@ def test_attn_sink_of_minus_infinity_is_no_sink(HQ, H, K, dt, new, ctx, mx):
         _status_ok()
 
 
+# ------------------------------------------------------------------ infinite values
+
+@pytest.mark.parametrize("window", [0, 60])
+@pytest.mark.parametrize("HQ,H,K,dt", ROUTES + [(4, 4, 128, BF), (3, 1, 128, BF)])
+@pytest.mark.parametrize("new,mx", [([1, 1], 1), ([5, 1, 8], 8), ([40, 1], None)])
+def test_attn_infinite_values(new, mx, HQ, H, K, dt, window):
+    """An infinite value is infinite in every row that sees its token, a NaN (or
+    infinities of both signs) NaN, and the other rows and channels stay."""
+    ctx = [100, 90, 33][:len(new)]
+    x, cu, kv, table = tp._attn_inputs(HQ, H, K, K, 64, dt, new, ctx)
+    kw = dict(max_new=mx, window_size=window)
+    clean, _ = _attn(x, cu, kv, table, **kw)
+    tol = 1e-5 if dt == F32 else 2e-2
+    cases = [(ctx[0] - 10, ctx[0] - 10), (kv[0] - 1, kv[0] - 1), (ctx[0] - 3, kv[0] - 1)]
+    if new[0] > 1:
+        cases.append((ctx[0] + 1, ctx[0] + 2))
+    pages = x["v_pages"].clone()
+    for j, j2 in cases:  # tokens of request 0
+        at = lambda j: (int(table[0, j // 64]), slice(None), j % 64)
+        x["v_pages"][(*at(j), 3)] = math.inf
+        x["v_pages"][(*at(j), 5)] = -math.inf
+        x["v_pages"][(*at(j), 7)] = math.nan
+        x["v_pages"][(*at(j), 9)] = math.inf
+        x["v_pages"][(*at(j2), 10)] = -math.inf
+        o, _ = _attn(x, cu, kv, table, **kw)
+        rows = np.arange(cu[-1])
+        pos = ctx[0] + rows
+        sees = lambda j: torch.tensor((rows < cu[1]) & (pos >= j) & (pos - j < (window or 1 << 30)))
+        s, s2 = sees(j).to(DEV), sees(j2).to(DEV)
+        assert (o[s][..., 3] == math.inf).all() and (o[s][..., 5] == -math.inf).all(), (j, j2)
+        assert torch.isnan(o[s][..., 7]).all() and (o[s][..., 9] == math.inf).all()
+        assert (o[s2][..., 10] == -math.inf).all()
+        for ch in range(K):
+            seen = {3: s, 5: s, 7: s, 9: s, 10: s2}.get(ch)
+            d = (o[..., ch].float() - clean[..., ch].float()).abs()
+            if seen is not None:
+                d = d[~seen]
+            assert d.numel() == 0 or d.max() <= tol, (j, j2, ch)
+        x["v_pages"].copy_(pages)
+    # infinities of both signs in one channel
+    j, j2 = ctx[0] - 3, kv[0] - 1
+    x["v_pages"][int(table[0, j // 64]), :, j % 64, 3] = math.inf
+    x["v_pages"][int(table[0, j2 // 64]), :, j2 % 64, 3] = -math.inf
+    o, _ = _attn(x, cu, kv, table, **kw)
+    assert torch.isnan(o[cu[1] - 1, :, 3]).all() and torch.isfinite(o[cu[1] - 1, :, 4:]).all()
+    _status_ok()
+
+
 # --------------------------------------------------------------- the largest batches
 
 def test_attn_flags_of_the_largest_batches():
