@@ -11,9 +11,10 @@
 // step of 2^-8, as a tensor-core operand has to be).  P is rounded to bf16
 // for P V; its sum is taken in fp32 before that.  A unit whose exponents
 // p_i + R_{page(i)} - R_I pass +-100 on some channel, or whose R_I - R_{page(j)}
-// passes +100, or whose result holds a NaN (a value that is not finite
-// reaches the rows that do not see it as 0 * inf), is flagged, and the general
-// kernel computes it again, exactly, behind this one.
+// passes +100, or whose result is not finite (a value that is not reaches the
+// rows that do not see it as 0 * inf; sums taken before a row's reference is
+// raised may pass fp32), is flagged, and the general kernel computes it again,
+// exactly, behind this one.
 //
 // Work.  One CTA per SM takes an even share of the batch's (unit, 128-key
 // tile) pairs in order (wall_paged.cuh): the tile pipeline's rings and
@@ -888,7 +889,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long row = (long)(s.t0 + r) * a.HQ + h;
         // each group writes half of the channels
         if (!idle) {
-          bool bad = false;  // a NaN: perhaps 0 * infinity or 0 * NaN of a masked value
+          // a NaN may be 0 * infinity or 0 * NaN of a masked value, an infinity a
+          // sum that passed fp32 before its reference was raised
+          bool bad = false;
 #pragma unroll 1
           for (int cc = grp * (V / 2); cc < (grp + 1) * (V / 2); cc += 32) {
             uint32_t ov0[32], ov1[32];
@@ -900,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               // (a row whose weight is 0 had no key in the group: its O is 0)
               float x = has0 ? __uint_as_float(ov0[e]) * f0 : 0.f;
               if (has1) x = fmaf(__uint_as_float(ov1[e]), f1, x);
-              bad |= x != x;
+              bad |= !(fabsf(x) < INFINITY);
               ov0[e] = __float_as_uint(x);
             }
             if (row_ok) {

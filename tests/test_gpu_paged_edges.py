@@ -179,6 +179,34 @@ def test_attn_infinite_values(new, mx, HQ, H, K, dt, window):
     _status_ok()
 
 
+# ------------------------------------------------------------- sums past the floats
+
+def test_attn_large_values_behind_a_jump():
+    """Scores that jump by 95 powers of two in a late tile over values of 2^34:
+    the sums before the reference is raised pass fp32, the result does not."""
+    HQ, H, K, PS, N = 16, 4, 64, 64, 40
+    new, ctx = [20] * N, [700] * N
+    x, _, _, _ = tp._attn_inputs(HQ, H, K, K, PS, BF, [20], [700], decay=0.0)
+    cu, kv = (np.arange(N + 1) * 20).tolist(), [720] * N
+    _, _, one, _, _ = tp._batch([20], [700], PS, 0)
+    table = np.repeat(one, N, 0)   # every request over the same pages
+    x["r_pages"].zero_()
+    x["k_pages"].zero_()
+    d = torch.zeros(K, device=DEV)
+    d[0] = 1.0
+    x["q"] = (d * 8.0).to(BF).repeat(20 * N, HQ, 1)
+    x["p"] = torch.zeros(20 * N, HQ, K, device=DEV)
+    for j in (300, 410):           # scale log2(e) * 8 * k = 95
+        x["k_pages"][int(one[0, j // PS]), :, j % PS] = (d * (95 / 1.4427 / 8 * K ** 0.5)).to(BF)
+    x["v_pages"] = (x["v_pages"].float() * 2.0 ** 34).to(BF)
+    want, _ = ref.attn(x["q"][:20], x["p"][:20], [0, 20], [720], torch.tensor(one), x["k_pages"],
+                       x["v_pages"], x["r_pages"], PS, K ** -0.5)
+    o, _ = _attn(x, cu, kv, table)
+    _status_ok()
+    assert torch.isfinite(o).all()
+    assert_fwd(BF, o.float() * 2.0 ** -34, np.tile(want * 2.0 ** -34, (N, 1, 1)))
+
+
 # --------------------------------------------------------------- the largest batches
 
 def test_attn_flags_of_the_largest_batches():
