@@ -168,7 +168,9 @@ __global__ void __launch_bounds__(kSlotThreads) slots_kernel(PlanArgs a) {
 }
 
 // Finished requests' pages back on the stack, in request order, each request's
-// in table order; their table rows become -1 and their lengths 0.
+// in table order; their table rows become -1 and their lengths 0.  An entry that
+// is no page is reported and dropped: a plan that opened it would lose tokens
+// of a request that has nothing to do with it.
 __global__ void __launch_bounds__(kPlanThreads, 1)
     release_kernel(const int* finished, int* lens, int* table, int* free_list, int* free_count,
                    int N, int MP, int NP, int shift, int* status) {
@@ -183,24 +185,37 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     const int i = i0 + threadIdx.x;
     const bool done = i < N && finished[i] != 0;
     const int held = done ? (int)min((long long)MP, ((long long)max(lens[i], 0) + PS1) >> shift) : 0;
-    long long tot;
-    const long long upto = before + block_incl_sum(held, sw, tot);
-    before += tot;
-    const long long at = upto - held;
-    if (done) lens[i] = 0;
-    unsigned many = __ballot_sync(0xffffffffu, held > 0);
-    while (many) {
-      const int src = __ffs(many) - 1;
-      many &= many - 1;
+    const unsigned some = __ballot_sync(0xffffffffu, held > 0);
+    int pages = 0;  // of the held entries
+    for (unsigned m = some; m; m &= m - 1) {
+      const int src = __ffs(m) - 1;
       const int cnt = __shfl_sync(0xffffffffu, held, src);
-      const long long a0 = __shfl_sync(0xffffffffu, at, src);
+      const int* row = table + (long)(i - lane + src) * MP;
+      int n = 0;
+      for (int x = lane; x < cnt; x += 32) n += (unsigned)row[x] < (unsigned)NP;
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (lane == src) pages = n;
+    }
+    long long tot;
+    const long long upto = before + block_incl_sum(pages, sw, tot);
+    before += tot;
+    const long long at = upto - pages;
+    if (done) lens[i] = 0;
+    for (unsigned m = some; m; m &= m - 1) {
+      const int src = __ffs(m) - 1;
+      const int cnt = __shfl_sync(0xffffffffu, held, src);
+      long long a0 = __shfl_sync(0xffffffffu, at, src);
       int* row = table + (long)(i - lane + src) * MP;
-      for (int x = lane; x < cnt; x += 32) {
-        const int id = row[x];
-        // more pages than the pool has, or an entry that is none: the table
-        // was not this stack's
-        if (a0 + x < NP) free_list[a0 + x] = id;
-        if (a0 + x >= NP || (unsigned)id >= (unsigned)NP) record_status(status, WALL_ERR_INVALID_ARG);
+      for (int x0 = 0; x0 < cnt; x0 += 32) {
+        const int x = x0 + lane, id = x < cnt ? row[x] : -1;
+        const unsigned good = __ballot_sync(0xffffffffu, (unsigned)id < (unsigned)NP);
+        const long long to = a0 + __popc(good & ((1u << lane) - 1));
+        a0 += __popc(good);
+        if (x >= cnt) continue;
+        // no page, or more of them than the pool has: the table was not this stack's
+        const bool page = (good >> lane) & 1u;
+        if (page && to < NP) free_list[to] = id;
+        else record_status(status, WALL_ERR_INVALID_ARG);
         row[x] = -1;
       }
     }

@@ -65,7 +65,8 @@ int wall_paged_plan(const int32_t* new_lens, const int32_t* lens, int32_t* block
 
 /* wall_paged_release -- pages of the requests with finished[i] != 0 back onto
  * the stack (request order, each in table order); their table entries become
- * -1 and their lens 0.  All arrays in place. */
+ * -1 and their lens 0.  All arrays in place.  A table entry outside the pool is
+ * no page: it records WALL_ERR_INVALID_ARG and is dropped. */
 int wall_paged_release(const int32_t* finished, int32_t* lens, int32_t* block_table,
                        int32_t* free_list, int32_t* free_count, int n_req, int max_pages,
                        int num_pages, int page_size, wall_stream_t stream);

@@ -207,6 +207,50 @@ def test_attn_large_values_behind_a_jump():
     assert_fwd(BF, o.float() * 2.0 ** -34, np.tile(want * 2.0 ** -34, (N, 1, 1)))
 
 
+# -------------------------------------------------------- pages that are none, release
+
+def test_release_keeps_entries_that_are_no_pages_off_the_stack():
+    """Table entries outside the pool are reported and dropped: the stack holds
+    pages alone, in the order of the table, and a later plan opens only them."""
+    PS, NP, MP = 32, 60, 60
+    for bad in (-1, NP, 2 ** 31 - 1, -2 ** 31):
+        tb = api.WallPagedTables(5, MP, NP, page_size=PS)
+        tb.plan(_i32([40, 1, 100, 0, 32 * 40]), 40 + 1 + 100 + 32 * 40)
+        _status_ok()
+        held = tb.block_table.tolist()
+        n_free = tb.free_count.item()
+        free = tb.free_list[:n_free].tolist()
+        tb.block_table[0, 1] = tb.block_table[2, 0] = tb.block_table[4, 35] = bad
+        tb.release(_i32([1, 0, 1, 0, 1]))
+        assert L.wall_get_status() == L.WALL_ERR_INVALID_ARG
+        back = [held[0][0]] + held[2][1:4] + held[4][:35] + held[4][36:40]
+        count = tb.free_count.item()
+        assert tb.free_list[:count].tolist() == free + back
+        assert tb.lens.tolist() == [0, 1, 0, 0, 0]
+        assert (tb.block_table[[0, 2, 4]] == -1).all()
+        # three pages are lost: one more than are left does not fit (nor does what
+        # needs a page behind it), all that are left do
+        plan = tb.plan(_i32([0, 0, 0, (count + 1) * PS, count * PS]), (2 * count + 1) * PS)
+        assert plan.admitted.tolist()[3:] == [0, 0]
+        plan = tb.plan(_i32([0, 0, 0, 0, count * PS]), count * PS)
+        assert plan.admitted.tolist()[3:] == [1, 1]
+        ids = tb.block_table[4, :count]
+        assert ((ids >= 0) & (ids < NP)).all() and len(set(ids.tolist())) == count
+        _status_ok()
+
+
+def test_release_more_pages_than_the_pool_has():
+    """Lengths that are not this stack's: reported, and the stack stays full at
+    most."""
+    tb = api.WallPagedTables(3, 4, 6, page_size=32)
+    tb.block_table.copy_(_i32([[0, 1, 2, 3], [4, 5, 0, 1], [2, 3, 4, 5]]))
+    tb.lens.fill_(128)
+    tb.free_count.zero_()
+    tb.release(_i32([1, 1, 1]))
+    assert L.wall_get_status() == L.WALL_ERR_INVALID_ARG
+    assert tb.free_count.item() == 6 and tb.free_list.tolist() == [0, 1, 2, 3, 4, 5]
+
+
 # --------------------------------------------------------------- the largest batches
 
 def test_attn_flags_of_the_largest_batches():
