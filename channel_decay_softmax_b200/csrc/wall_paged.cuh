@@ -339,6 +339,19 @@ struct PartDesc {
   int last_cta;     // < 0: this CTA begins no unit that another one ends
 };
 
+// A scaled query's channel x as an operand, y = x 2^e: finite where x is, at most
+// the largest bf16 number.  Growth by 2^128 and more from a page to a row (whose
+// keys there count 2^27 fold at least) then adds nothing where the query or the
+// key is 0, instead of 0 * inf.  The callers look for such growth in a vector of
+// channels first: done for each channel, this cost drafts 8 % and fp32 rows 5 %.
+constexpr float kMostQuery = 3.38953139e38f;
+__device__ __forceinline__ float bound_query(float y, float x) {
+  return fabsf(y) > kMostQuery && fabsf(x) < INFINITY ? copysignf(kMostQuery, y) : y;
+}
+__device__ __forceinline__ float grown_query(float x, float e) {
+  return bound_query(x * exp2f(e > 127.f ? 127.f : e), x);
+}
+
 // 2^(sink - m), in log2: a sink of -inf is none, also beside m = -inf (a row that
 // sees nothing).
 __device__ __forceinline__ float sink_weight(float sink, float m) {

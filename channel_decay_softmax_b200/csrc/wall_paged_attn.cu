@@ -120,9 +120,20 @@ __device__ __forceinline__ void gen_tiles(const AttnArgs& a, const Request& r, i
         const int d[8] = {u0.x - w0.x, u0.y - w0.y, u0.z - w0.z, u0.w - w0.w,
                           u1.x - w1.x, u1.y - w1.y, u1.z - w1.z, u1.w - w1.w};
         const bool sees = rs >= slot;
+        float most = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          qv[e] = sees ? a.scale_log2 * qv[e] * exp2f(pv[e] + (float)d[e]) : 0.f;
+        for (int e = 0; e < 8; ++e) {
+          pv[e] += (float)d[e];
+          most = fmaxf(most, pv[e]);
+          qv[e] *= a.scale_log2;
+        }
+        if (most <= kPageRange) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) qv[e] = sees ? qv[e] * exp2f(pv[e]) : 0.f;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) qv[e] = sees ? grown_query(qv[e], pv[e]) : 0.f;
+        }
         store8(sQ + row * K + c, qv);
       }
       at = slot;

@@ -313,8 +313,13 @@ __global__ void __launch_bounds__(288, 1)
             __syncwarp();
   #pragma unroll
             for (int y = 0; y < QPL; y += 2) {
-              float x0 = qv[y] * exp2f(pv[y] + (float)(Rq[y] - R[y]));
-              float x1 = qv[y + 1] * exp2f(pv[y + 1] + (float)(Rq[y + 1] - R[y + 1]));
+              const float e0 = pv[y] + (float)(Rq[y] - R[y]);
+              const float e1 = pv[y + 1] + (float)(Rq[y + 1] - R[y + 1]);
+              float x0 = qv[y] * exp2f(e0), x1 = qv[y + 1] * exp2f(e1);
+              if (fmaxf(e0, e1) > kPageRange) {
+                x0 = grown_query(qv[y], e0);
+                x1 = grown_query(qv[y + 1], e1);
+              }
               const int ch = lane * QPL + y, pair = (ch & 15) >> 1;
               uint8_t* w = qt + (pair & 3) * 3 * kQGroup + ((ch >> 4) * 2 + (pair >> 2)) * 4;
   #pragma unroll
@@ -473,12 +478,19 @@ __global__ void __launch_bounds__(288, 1)
           if ((j0 >> a.shift) != page_at) {
             page_at = j0 >> a.shift;
             const int* R = reinterpret_cast<const int*>(sb + oR) + g * KD + r0;
+            float most = 0.f;
 #pragma unroll
             for (int y = 0; y < KD / 8; ++y) {
               const int2 rc = *reinterpret_cast<const int2*>(R + y * 8);
               const int2 ro = *reinterpret_cast<const int2*>(Rq + y * 8);
               const float x0 = times_pow2(xq[y].x, ro.x - rc.x), x1 = times_pow2(xq[y].y, ro.y - rc.y);
+              most = fmaxf(most, fmaxf(fabsf(x0), fabsf(x1)));
               qh[y] = pack2(x0, x1);
+            }
+            if (most > kMostQuery) {
+#pragma unroll
+              for (int y = 0; y < KD / 8; ++y)
+                qh[y] = pack2(bound_query(low_of(qh[y]), xq[y].x), bound_query(high_of(qh[y]), xq[y].y));
             }
           }
           // scores of keys quad + 8 i

@@ -34,6 +34,8 @@ extern "C" {
  *   2^(P_t - P_j) k_j = 2^(p_t + R_{page(t)} - R_c) * (k_pages row of j).
  * |p_t| > 100 on some channel (a page whose gates sum past 100 powers of two)
  * cannot be stored and records WALL_ERR_RANGE; smaller pages reach further.
+ * Gates may have either sign.  A query's factor 2^(p_t + R_{page(t)} - R_c) of
+ * 2^127 and more counts as 2^127.
  * A row offset, slot or page id outside its array is never followed: it
  * records WALL_ERR_INVALID_ARG (wall_get_status) and what hangs on it is
  * unspecified.  int32 and int64 arrays are aligned to their element, the

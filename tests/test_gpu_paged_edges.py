@@ -106,6 +106,30 @@ def test_attn_long_zigzag():
     assert_fwd(BF, o, want, lse, lse_want)
 
 
+# -------------------------------------------------------------- growth past fp32
+
+@pytest.mark.parametrize("PS", [32, 64])
+@pytest.mark.parametrize("HQ,H,K,dt", ROUTES)
+@pytest.mark.parametrize("new", [1, 8, 40])
+def test_attn_growth_past_the_floats(new, HQ, H, K, dt, PS):
+    """Channels that gain 80 powers of two a page, up to 2^200 and more between
+    a key and a row, where the query or the key is 0: they add nothing."""
+    gen = torch.Generator().manual_seed(new + PS)
+    n = 2 * PS + 60
+    t = torch.arange(n).float()
+    P = (-0.02 * t)[:, None, None].repeat(1, HQ, K)
+    P[:, :, ::4] = (80.0 / PS * t)[:, None, None]
+    q, k = torch.randn(new, HQ, K, generator=gen), torch.randn(n, HQ, K, generator=gen)
+    q[:, :, ::8] = 0
+    k[:, :, 4::8] = 0
+    x, cu, kv, table = _cache_of(P, q, k, new, H, K, PS, dt)
+    want, lse_want = ref.attn(x["q"], x["p"], cu, kv, torch.tensor(table), x["k_pages"],
+                              x["v_pages"], x["r_pages"], PS, K ** -0.5)
+    o, lse = _attn(x, cu, kv, table, max_new=new)
+    _status_ok()
+    assert_fwd(dt, o, want, lse, lse_want)
+
+
 # ------------------------------------------------------------------ infinite sinks
 
 @pytest.mark.parametrize("HQ,H,K,dt", ROUTES)
