@@ -298,3 +298,68 @@ def test_attn_flags_of_the_largest_batches():
     assert torch.equal(got[:n - 1], want[:n - 1]) and torch.isnan(got[n - 1]).all()
     del got
     torch.cuda.empty_cache()
+
+
+# -------------------------------------------------- forms that other cases pass by
+
+@pytest.mark.parametrize("HQ,H,K,V", [(1, 1, 128, 128), (4, 1, 128, 64), (6, 1, 64, 128),
+                                      (8, 1, 128, 128), (4, 4, 64, 64)])
+def test_attn_single_rows_do_not_see_past_their_window(HQ, H, K, V):
+    """Keys and values just before the window, in the tile that it begins in,
+    may be anything: the same bits."""
+    ctx, window = [100, 500, 63, 31], 40
+    x, cu, kv, table = tp._attn_inputs(HQ, H, K, V, 64, BF, [1] * 4, ctx)
+    clean = _attn(x, cu, kv, table, max_new=1, window_size=window)
+    for bad in (math.nan, math.inf, -math.inf):
+        for i, n in enumerate(kv):
+            for j in range(max(0, n - window - 20), n - window):
+                x["v_pages"][int(table[i, j // 64]), :, j % 64] = bad
+                x["k_pages"][int(table[i, j // 64]), :, j % 64] = bad
+        got = _attn(x, cu, kv, table, max_new=1, window_size=window)
+        assert torch.equal(got[0], clean[0]) and torch.equal(got[1], clean[1])
+    _status_ok()
+
+
+@pytest.mark.parametrize("hint", [False, True])
+@pytest.mark.parametrize("case", [
+    (4, 2, 64, 64, 64, F32, [900, 2, 411], [100, 640, 0]),
+    (2, 1, 40, 24, 32, F32, [600, 1, 0, 300], [31, 7, 5, 0]),
+    (3, 3, 128, 64, 128, F32, [1100, 129], [127, 0]),
+    (2, 1, 64, 64, 128, F32, [40, 129, 1], [100, 0, 300]),
+    (2, 2, 64, 128, 128, BF, [1000, 3], [5, 128])])
+def test_append_run_by_run_in_every_form(case, hint):
+    """Prompts of more than four blocks in fp32 and over pages of 128."""
+    tp.test_append(case, hint)
+
+
+@pytest.mark.parametrize("dt,K,signed,sink,window", [(BF, 128, True, False, 0), (BF, 64, False, True, 0),
+                                                     (F32, 64, True, True, 90), (BF, 128, True, True, 50)])
+def test_serving_run_with_sink_and_signed_gates(dt, K, signed, sink, window):
+    """A prompt, single tokens, drafts and a chunk of one request, beside
+    another: every row equals the oracle's forward of the whole sequence."""
+    HQ, H, PS = 4, 2, 64
+    gen = torch.Generator().manual_seed(17)
+    lens = [260, 150]
+    sk = torch.randn(HQ, generator=gen) if sink else None
+    seqs = []
+    for n in lens:
+        g = tp._rand(gen, n, HQ, K, dtype=dt, amp=0.04)
+        seqs.append(dict(q=tp._rand(gen, n, HQ, K, dtype=dt), k=tp._rand(gen, n, H, K, dtype=dt),
+                         v=tp._rand(gen, n, H, K, dtype=dt), g=g if signed else -g.abs()))
+    want = [wo.forward(*(s[n][None].cpu() for n in "qkvg"), scale=K ** -0.5, sink_bias=sk,
+                       window_size=window or None)[0][0] for s in seqs]
+    tb = api.WallPagedTables(2, 5, 10, page_size=PS)
+    cache = api.WallPagedCache(tb, H, HQ, K, K, dtype=dt, window_size=window or None,
+                               sink_bias=None if sk is None else sk.to(DEV))
+    at = [0, 0]
+    for new in ([130, 1], [1, 60], [1, 1], [8, 3], [60, 1], [1, 84], [59, 0]):
+        cat = {x: torch.cat([s[x][a:a + n] for s, a, n in zip(seqs, at, new)]) for x in "qkvg"}
+        o = cache.step(tb.plan(_i32(new), sum(new)), cat["q"], cat["k"], cat["v"], cat["g"],
+                       max_new=max(new))
+        r0 = 0
+        for i, n in enumerate(new):
+            assert_fwd(dt, o[r0:r0 + n], want[i][at[i]:at[i] + n], what=f"request {i}")
+            at[i] += n
+            r0 += n
+    assert at == lens
+    _status_ok()
