@@ -91,8 +91,9 @@ static_assert(kNumBars <= DSmem<128>::kBars, "barrier slots");
 static_assert(DSmem<128>::kAlloc <= 227 * 1024, "shared memory");
 
 // 2^k as bf16 bits for an integer k (the anchors are integers): exact in
-// the normal range, 0 below it (a factor under 2^-126 scales a key that
-// decays to nothing) and +inf above it, as the fp32 product would overflow.
+// the normal range, 0 below it (what a factor under 2^-126 leaves counts as
+// nothing: see kAnchorRange) and +inf above it, as the fp32 product would
+// overflow.
 __device__ __forceinline__ uint32_t pow2_bf16(float k) {
   const int e = (int)k;
   return e < -126 ? 0u : e > 127 ? 0x7F80u : uint32_t(e + 127) << 7;

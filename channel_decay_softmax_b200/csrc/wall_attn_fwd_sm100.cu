@@ -138,8 +138,9 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 }
 
 // 2^k as bf16 bits for an integer k (the anchors are integers): exact in
-// the normal range, 0 below it (a factor under 2^-126 scales a key that
-// decays to nothing) and +inf above it, as the fp32 product would overflow.
+// the normal range, 0 below it (what a factor under 2^-126 leaves counts as
+// nothing: see kAnchorRange) and +inf above it, as the fp32 product would
+// overflow.
 __device__ __forceinline__ uint32_t pow2_bf16(float k) {
   const int e = (int)k;
   return e < -126 ? 0u : e > 127 ? 0x7F80u : uint32_t(e + 127) << 7;
@@ -704,9 +705,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // preparation: anchored operands Qh, Kh (per query head) and block anchors.
 // An anchored exponent |P - R| beyond kAnchorRange (a channel whose gate
-// sums past 2^kAnchorRange inside one block) flags its (sequence, head) unit
-// in `units`, which the SIMT kernels then recompute, or records
-// WALL_ERR_RANGE in `status` (the chunk call, which has no such fallback).
+// sums past 2^kAnchorRange inside one block), or a rise and a fall that pass it
+// together (note_range), flags its (sequence, head) unit in `units`, which the
+// SIMT kernels then recompute; the chunk call, which has no such fallback,
+// records WALL_ERR_RANGE in `status` for the first.
 
 __global__ void anchor_operands_kernel(const __nv_bfloat16* __restrict__ q,
                                        const __nv_bfloat16* __restrict__ k,
@@ -744,19 +746,16 @@ __global__ void anchor_operands_kernel(const __nv_bfloat16* __restrict__ q,
       float pv[8], rv[8], x[8], y[8];
       load8(P + (row * HQ + hh) * K + g8 * 8, pv);
       load8(P + (arow * HQ + hh) * K + g8 * 8, rv);
-      bool wide = false;
+      float rise = 0.f, fall = 0.f;
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         rv[c] = floorf(rv[c]);
-        wide |= fabsf(pv[c] - rv[c]) > kAnchorRange;
+        rise = fmaxf(rise, pv[c] - rv[c]);
+        fall = fmaxf(fall, rv[c] - pv[c]);
       }
-      if (wide) {
-        if (units) {
-          set_flag(units + (long)s * HQ + hh);
-          set_flag(units + (long)seqs.n * HQ);  // some unit is flagged
-        }
-        record_status(status, WALL_ERR_RANGE);
-      }
+      if (units)
+        note_range(units, (long)s * HQ + hh, (long)seqs.n * HQ, rise, fall, kAnchorRange, kMinorRange);
+      if (fmaxf(rise, fall) > kAnchorRange) record_status(status, WALL_ERR_RANGE);
       load8(q + (row * HQ + hh) * K + g8 * 8, x);
 #pragma unroll
       for (int c = 0; c < 8; ++c) y[c] = saturate_bf16(x[c] * exp2f(pv[c] - rv[c]));

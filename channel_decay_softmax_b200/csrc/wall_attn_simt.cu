@@ -65,7 +65,7 @@ __device__ __forceinline__ bool simt_item(const AttnProblem& pb, int item, bool 
   h = item % pb.HQ;
   const int b = item / pb.HQ;
   if (!seq_block(pb.seqs, BM, reverse ? pb.max_blocks64 - 1 - b : b, seq, blk)) return false;
-  return pb.units == nullptr || pb.units[(long)seq * pb.HQ + h] != 0;
+  return pb.units == nullptr || (pb.units[(long)seq * pb.HQ + h] & kUnitBeyond) != 0;
 }
 
 // dst[r][n] = src[row0+r, src_head, n] * exp2(sign * (P[row0+r, h, n] - R[n]))

@@ -53,6 +53,32 @@ __device__ __forceinline__ void set_flag(int* f) {
   if (*reinterpret_cast<volatile int*>(f) == 0) atomicOr(f, 1);
 }
 
+// Notes how far anchored exponents of a unit reach above and below 0 (rise, fall;
+// see kAnchorRange in wall_internal.h): `units` as TcFwdWs has them.  A unit's word
+// holds, above kUnitBeyond, its largest rise and fall in steps of 6 beyond
+// `minor`, each as so many set bits: an atomic OR is their maximum, and of two
+// threads that raise one each the later sees both.
+constexpr int kUnitBeyond = 1;
+__device__ __forceinline__ void note_range(int* units, long unit, long n_units, float rise,
+                                           float fall, float range, float minor) {
+  bool beyond = fmaxf(rise, fall) > range;
+  if (fmaxf(rise, fall) > minor) {
+    auto steps = [&](float x) { return (int)fminf(fmaxf(ceilf((x - minor) / 6.f), 0.f), 15.f); };
+    const int mine = ((1 << steps(rise)) - 1) << 1 | ((1 << steps(fall)) - 1) << 16;
+    if (mine & ~*reinterpret_cast<volatile int*>(units + unit)) {
+      const int all = atomicOr(units + unit, mine) | mine;
+      const int r = __popc(all & 0xfffe), f = __popc(all & 0x7fff0000);
+      // at most minor + 6 r and minor + 6 f
+      beyond |= r > 0 && f > 0 && minor + 6.f * (r + f) > range;
+    }
+  }
+  if (beyond) {
+    if (!(*reinterpret_cast<volatile int*>(units + unit) & kUnitBeyond))
+      atomicOr(units + unit, kUnitBeyond);
+    set_flag(units + n_units);  // some unit is flagged
+  }
+}
+
 // ---------------------------------------------------------------------------
 // element conversion
 

@@ -95,17 +95,21 @@ struct TcFwdWs {
   __nv_bfloat16* kh;   // [rows, HQ, K]  k * 2^(R_block - P)
   float* anchors;      // [n_blocks128, HQ, K]  P at each 128-row block start
   int n_blocks128;     // upper bound on 128-row blocks over all sequences
-  // [n_seq * HQ + 1]: nonzero for a (sequence, head) unit some of whose
-  // anchored exponents |P - R_block| exceed kAnchorRange, and in the last
-  // word if any unit is; the operand pass sets them, the SIMT kernels
-  // recompute those units
+  // [n_seq * HQ + 1], set by the operand pass (note_range): kUnitBeyond in the
+  // word of a (sequence, head) unit beyond the anchored range, and in the last
+  // word if any unit is.  The SIMT kernels recompute those units.
   int* units;
 };
-// Anchored exponents of the tensor-core operands stay within +-kAnchorRange:
-// Qh, Kh and every per-tile rescaled key then stay normal bf16 numbers for
-// inputs up to 2^20 in magnitude, and the products the MMAs form are exact
-// to bf16 rounding.
+// Anchored exponents P - R_block of the tensor-core operands stay within
+// +-kAnchorRange: Qh and Kh then stay normal bf16 numbers for inputs up to 2^20
+// in magnitude, and the products the MMAs form are exact to bf16 rounding.  A
+// tile's factor 2^(R_I - R_J) counts as 0 below 2^-126; what is lost so of a
+// product of a row that has risen by M above its block's anchor and a key that
+// has fallen by m below its own is at most 2^(M + m - 127) |q k|.  Gates <= 0
+// have M < 1; a unit whose M and m may pass kAnchorRange + kMinorRange together (a
+// loss of 2^-14, against the operands' rounding of 2^-9) is beyond the range too.
 constexpr float kAnchorRange = 100.f;
+constexpr float kMinorRange = 13.f;
 bool fwd_tc_supported(const AttnProblem& pb);
 int attn_prepare_operands(const AttnProblem& pb, const void* q, const void* k, const float* P,
                           const TcFwdWs& ws, cudaStream_t stream);

@@ -281,7 +281,7 @@ __device__ __forceinline__ void storew(float* p, const float* in) {
 //   Qh = q * 2^(P - R),  Kh = k * 2^(R - P),  R = floor(P at the row's
 //   128-row block start)   (the anchors, written at the block start row)
 // as the forward's preparation kernel forms them, flagging the (sequence,
-// head) units with an exponent |P - R| beyond kAnchorRange as it does.  R of a block whose start
+// head) units beyond the anchored range as it does.  R of a block whose start
 // lies in an earlier chunk is that row's prefix, rebuilt from its chunk's
 // carry: the scan's first step is carry + g, then one fused rounding.
 // The carries come from a scratch that is not P, so no thread reads a carry
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreadsScan, 4)
       cmp[v] = 0.f;
     }
   }
-  bool wide = false;  // some exponent of this thread's rows beyond kAnchorRange
+  float rise = 0.f, fall = 0.f;  // how far this thread's exponents reach
 #pragma unroll
   for (int r0 = 0; r0 < kChunk; r0 += kInFlightOps) {
     float a[kInFlightOps][VW], qa[kInFlightOps][VW], ka[kInFlightOps][VW];
@@ -375,7 +375,8 @@ __global__ void __launch_bounds__(kThreadsScan, 4)
 #pragma unroll
         for (int v = 0; v < VW; ++v) {
           e[v] = o[v] - R[v];
-          wide |= fabsf(e[v]) > kAnchorRange;
+          rise = fmaxf(rise, e[v]);
+          fall = fmaxf(fall, -e[v]);
           y[v] = saturate_bf16(qa[rr][v] * exp2f(e[v]));
         }
         storew<VW>(qh + pr * C + col, y);
@@ -387,10 +388,7 @@ __global__ void __launch_bounds__(kThreadsScan, 4)
       }
     }
   }
-  if (wide) {
-    set_flag(units + (long)s * HQ + hh);
-    set_flag(units + (long)seqs.n * HQ);  // some unit is flagged
-  }
+  note_range(units, (long)s * HQ + hh, (long)seqs.n * HQ, rise, fall, kAnchorRange, kMinorRange);
 }
 
 // The backward's dq finalize fused with pass 1 of the reverse scan of dL
@@ -423,7 +421,7 @@ __global__ void __launch_bounds__(kThreadsScan, 4)
   const int n = (int)min((long)kChunk, len - lr0);
   const int hh = (int)(col / K), n0 = (int)(col % K);
   const int G = HQ / H;
-  const bool final_dq = units[(long)s * HQ + hh] != 0;
+  const bool final_dq = (units[(long)s * HQ + hh] & kUnitBeyond) != 0;
   float sum[VW], cmp[VW];
 #pragma unroll
   for (int v = 0; v < VW; ++v) sum[v] = cmp[v] = 0.f;
