@@ -171,57 +171,83 @@ __global__ void __launch_bounds__(kSlotThreads) slots_kernel(PlanArgs a) {
 // in table order; their table rows become -1 and their lengths 0.  An entry that
 // is no page is reported and dropped: a plan that opened it would lose tokens
 // of a request that has nothing to do with it.
+//
+// The held entries of 1024 requests lie in one order, 8192 a round, and the pages
+// among them are counted before any is stored.  64 requests of 60 pages 4.2 us,
+// 1000 of 30 20.5, 4 of 1000 6.1.  (A warp for each request's entries, one request
+// after the other: 30, 33 and 21 with the pages counted first, 20, 18 and 27 when
+// they were not.)
+constexpr int kReleaseEach = 8;
 __global__ void __launch_bounds__(kPlanThreads, 1)
     release_kernel(const int* finished, int* lens, int* table, int* free_list, int* free_count,
                    int N, int MP, int NP, int shift, int* status) {
   __shared__ long long sw[32];
-  const int lane = threadIdx.x & 31;
+  __shared__ long long s_end[kPlanThreads];  // held entries up to and with each request
+  __shared__ int s_pages[32];
+  const int tid = threadIdx.x, lane = tid & 31;
   const int PS1 = (1 << shift) - 1;
   int n_free = *free_count;
-  if (threadIdx.x == 0 && (n_free < 0 || n_free > NP)) record_status(status, WALL_ERR_INVALID_ARG);
+  if (tid == 0 && (n_free < 0 || n_free > NP)) record_status(status, WALL_ERR_INVALID_ARG);
   n_free = min(max(n_free, 0), NP);
   long long before = n_free;
   for (int i0 = 0; i0 < N; i0 += kPlanThreads) {
-    const int i = i0 + threadIdx.x;
+    const int i = i0 + tid;
     const bool done = i < N && finished[i] != 0;
     const int held = done ? (int)min((long long)MP, ((long long)max(lens[i], 0) + PS1) >> shift) : 0;
-    const unsigned some = __ballot_sync(0xffffffffu, held > 0);
-    int pages = 0;  // of the held entries
-    for (unsigned m = some; m; m &= m - 1) {
-      const int src = __ffs(m) - 1;
-      const int cnt = __shfl_sync(0xffffffffu, held, src);
-      const int* row = table + (long)(i - lane + src) * MP;
-      int n = 0;
-      for (int x = lane; x < cnt; x += 32) n += (unsigned)row[x] < (unsigned)NP;
-      n = __reduce_add_sync(0xffffffffu, n);
-      if (lane == src) pages = n;
-    }
-    long long tot;
-    const long long upto = before + block_incl_sum(pages, sw, tot);
-    before += tot;
-    const long long at = upto - pages;
     if (done) lens[i] = 0;
-    for (unsigned m = some; m; m &= m - 1) {
-      const int src = __ffs(m) - 1;
-      const int cnt = __shfl_sync(0xffffffffu, held, src);
-      long long a0 = __shfl_sync(0xffffffffu, at, src);
-      int* row = table + (long)(i - lane + src) * MP;
-      for (int x0 = 0; x0 < cnt; x0 += 32) {
-        const int x = x0 + lane, id = x < cnt ? row[x] : -1;
-        const unsigned good = __ballot_sync(0xffffffffu, (unsigned)id < (unsigned)NP);
-        const long long to = a0 + __popc(good & ((1u << lane) - 1));
-        a0 += __popc(good);
-        if (x >= cnt) continue;
+    long long total;
+    const long long end = block_incl_sum(held, sw, total);
+    s_end[tid] = end;
+    __syncthreads();
+    for (long long e0 = 0; e0 < total; e0 += kPlanThreads * kReleaseEach) {
+      // a warp's entries of the round are neighbours, 32 at a time
+      const long long w0 = e0 + (long long)(tid & ~31) * kReleaseEach + lane;
+      int* at[kReleaseEach];
+      int id[kReleaseEach];
+      int r = 0;  // the requests that end at or before the entry
+#pragma unroll
+      for (int step = kPlanThreads / 2; step > 0; step >>= 1)
+        if (s_end[r + step - 1] <= w0) r += step;
+#pragma unroll
+      for (int x = 0; x < kReleaseEach; ++x) {
+        const long long e = w0 + 32 * x;
+        while (e < total && s_end[r] <= e) ++r;
+        at[x] = e < total ? table + (long)(i0 + r) * MP + (e - (r > 0 ? s_end[r - 1] : 0)) : nullptr;
+      }
+#pragma unroll
+      for (int x = 0; x < kReleaseEach; ++x) id[x] = at[x] ? *at[x] : -1;
+      unsigned page[kReleaseEach];
+      int n = 0;  // pages among the warp's entries
+#pragma unroll
+      for (int x = 0; x < kReleaseEach; ++x) {
+        page[x] = __ballot_sync(0xffffffffu, (unsigned)id[x] < (unsigned)NP);
+        n += __popc(page[x]);
+      }
+      if (lane == 0) s_pages[tid >> 5] = n;
+      __syncthreads();
+      int upto = s_pages[lane];
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += y;
+      }
+      long long to = before + __shfl_sync(0xffffffffu, upto, tid >> 5) - n;
+      before += __shfl_sync(0xffffffffu, upto, 31);
+      __syncthreads();  // s_pages has been read
+#pragma unroll
+      for (int x = 0; x < kReleaseEach; ++x) {
+        const long long mine = to + __popc(page[x] & ((1u << lane) - 1));
+        to += __popc(page[x]);
+        if (!at[x]) continue;
+        *at[x] = -1;
         // no page, or more of them than the pool has: the table was not this stack's
-        const bool page = (good >> lane) & 1u;
-        if (page && to < NP) free_list[to] = id;
+        if (((page[x] >> lane) & 1u) && mine < NP) free_list[mine] = id[x];
         else record_status(status, WALL_ERR_INVALID_ARG);
-        row[x] = -1;
       }
     }
+    __syncthreads();  // s_end has been read
   }
-  __syncthreads();
-  if (threadIdx.x == 0) *free_count = (int)min(before, (long long)NP);
+  if (tid == 0) *free_count = (int)min(before, (long long)NP);
 }
 
 }  // namespace
