@@ -718,6 +718,10 @@ class WallPagedCache:
         cache = WallPagedCache(tables, H, HQ, K, V)          # one per layer
         plan = tables.plan(new_lens, n_tokens)                # once a step
         o = cache.step(plan, q, k, v, g)                      # each layer
+
+    A step of single tokens passes max_new=1: the lengths are on the GPU, so
+    without a bound every request may have all n_tokens rows, and the call runs
+    the kernels for longer requests as well.
     """
 
     def __init__(self, tables, H, HQ, K, V, dtype=torch.bfloat16, scale=None, sink_bias=None,

@@ -9,11 +9,11 @@
 // the key row go out (bf16), with k and v shared by a group: memory-bound.
 // Three ways, by how many tokens a request may bring:
 //   one     a warp takes a request's 128 channels: no scan at all
-//   few     a CTA takes one request and 128 channels and walks the tokens in
-//           blocks aligned to the pages, sixteen warps each: every warp sums
-//           its own tokens' gates, the sums are scanned in shared memory, and
-//           each warp then forms its tokens from its own prefix -- three
-//           barriers a block, its loads all in flight at once
+//   few     a CTA takes one request and 64 channels and walks the tokens in
+//           blocks aligned to the pages, shared by sixteen half-warps: every one
+//           sums its own tokens' gates, the sums are scanned in shared memory, and
+//           each then forms its tokens from its own prefix -- three barriers a
+//           block, its loads all in flight at once
 //   many    the blocks ("runs") side by side: a pass over g leaves each run's
 //           sums, a scan over a request's runs makes them prefixes (exact in
 //           any order, being integers), and the same kernel forms each run

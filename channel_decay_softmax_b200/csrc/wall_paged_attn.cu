@@ -26,7 +26,9 @@ using namespace paged;
 // is kept by lanes until the end.  Measured: six fp32 requests of up to 70 rows
 // over up to 970 keys (K = V = 64) 30 us, from 68: a tile's chain of page, load,
 // scores and P V is what is left, three CTAs a SM to cover it (lines of the next
-// tile sent ahead to the L2 gain nothing).
+// tile sent ahead to the L2 gain nothing).  Three CTAs leave a thread 168
+// registers, over which the forms of this kernel and of flagged_kernel spill up
+// to 96 bytes.
 
 constexpr int GR = kGeneralRows;
 constexpr int kGenWarps = 4, kGenThreads = kGenWarps * 32;

@@ -22,8 +22,8 @@
 // last ones balance to within a tile, and a few rows over a long context
 // spread over all SMs and are joined afterwards.
 //
-// Measured: an 8192-token prompt of 16 heads in 372 us, 739 TFLOP/s of its
-// visible pairs (45 % of the dense bf16 rate).  A tile takes 2600 cycles where
+// Measured: an 8192-token prompt of 16 heads in 399 us with the queries' pass and
+// the join, 689 TFLOP/s of its visible pairs (42 % of the dense bf16 rate).  A tile takes 2600 cycles where
 // its MMAs are worth 1024 and its operands, copies and rescale hold the shared
 // memory for 1800: the thread that issues the MMAs waits for S's keys, P and V
 // in turn, and what it has issued runs out meanwhile.  Units of a few tiles
@@ -68,7 +68,9 @@ constexpr float kFlagAbove = 1.2676506e30f;  // 2^100: one that may not be held
 // product is below 2^(kRise + 100 - 127) |q k| and counts as 0.  In a unit whose
 // rows rise further the factor is applied in two steps instead.
 constexpr float kRise = 1.f;
-// A unit's own cost, in tiles (an 8192-token prompt: 398 us; 2: 404, 4: 402)
+// A unit's own cost, in tiles.  An 8192-token prompt, windowed chunks and a mixed
+// step take 399, 92.0 and 129.6 us; with 2: 406, 92.1, 130.4; with 4: 404, 91.6,
+// 129.1; with 6: 413, 91.9, 127.7.
 constexpr int kUnit = 3;
 
 // The walk over the units as calls: it runs once a unit or less, and the code of
@@ -670,8 +672,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     mul_bf16x2(w[x].z, f2), mul_bf16x2(w[x].w, f3));
           }
         };
-        // a shared-memory load takes hundreds of cycles while the tensor core
-        // streams its operands: the next 32 rows are always in flight
+        // A shared-memory load takes hundreds of cycles while the tensor core
+        // streams its operands: 32 rows (KD / 16 vectors a thread) are loaded
+        // before the first is scaled.
 #pragma unroll 1
         for (int z = 0; z < 4; ++z) {
           uint4 wa[kBatch];

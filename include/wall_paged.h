@@ -38,8 +38,9 @@ extern "C" {
  * 2^127 and more counts as 2^127.
  * A row offset, slot or page id outside its array is never followed: it
  * records WALL_ERR_INVALID_ARG (wall_get_status) and what hangs on it is
- * unspecified.  int32 and int64 arrays are aligned to their element, the
- * others to 16 bytes.  Limits: n_req <= 2^20, HQ <= 4096, num_pages *
+ * unspecified.  r_pages, carry_in, carry_out and the arrays of `dtype` and fp32
+ * values are aligned to 16 bytes (sink_bias and lse to 4), the other int32 and
+ * int64 arrays to their element.  Limits: n_req <= 2^20, HQ <= 4096, num_pages *
  * page_size * HQ < 2^31.
  */
 
