@@ -64,8 +64,14 @@ __device__ __forceinline__ void note_range(int* units, long unit, long n_units, 
   bool beyond = fmaxf(rise, fall) > range;
   if (fmaxf(rise, fall) > minor) {
     auto steps = [&](float x) { return (int)fminf(fmaxf(ceilf((x - minor) / 6.f), 0.f), 15.f); };
-    const int mine = ((1 << steps(rise)) - 1) << 1 | ((1 << steps(fall)) - 1) << 16;
-    if (mine & ~*reinterpret_cast<volatile int*>(units + unit)) {
+    // one lane for those of the warp that are at the same unit: where every
+    // thread's channels fall far, the words would be what all of them wait for
+    // (a forward with g about -0.3: 449 us for 412)
+    const unsigned same = __match_any_sync(__activemask(), (unsigned long long)unit);
+    const int mine = (int)__reduce_or_sync(
+        same, ((1 << steps(rise)) - 1) << 1 | ((1 << steps(fall)) - 1) << 16);
+    if ((int)(threadIdx.x & 31) == __ffs(same) - 1 &&
+        (mine & ~*reinterpret_cast<volatile int*>(units + unit))) {
       const int all = atomicOr(units + unit, mine) | mine;
       const int r = __popc(all & 0xfffe), f = __popc(all & 0x7fff0000);
       // at most minor + 6 r and minor + 6 f
