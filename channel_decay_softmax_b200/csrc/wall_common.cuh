@@ -66,7 +66,7 @@ __device__ __forceinline__ void note_range(int* units, long unit, long n_units, 
     auto steps = [&](float x) { return (int)fminf(fmaxf(ceilf((x - minor) / 6.f), 0.f), 15.f); };
     // one lane for those of the warp that are at the same unit: where every
     // thread's channels fall far, the words would be what all of them wait for
-    // (a forward with g about -0.3: 449 us for 412)
+    // (a forward of 8192 tokens with g about -0.3: 449 us for 412)
     const unsigned same = __match_any_sync(__activemask(), (unsigned long long)unit);
     const int mine = (int)__reduce_or_sync(
         same, ((1 << steps(rise)) - 1) << 1 | ((1 << steps(fall)) - 1) << 16);
